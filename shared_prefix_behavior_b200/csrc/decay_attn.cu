@@ -131,15 +131,16 @@ __device__ __forceinline__ DecayUser user_at(const DecayArgs& a, int u) {
 //
 // An operand is one bf16 number (bf16 calls) or the exact sum of three (fp32
 // calls: 8 + 8 + 8 significant bits), and a product sums the pairs of terms
-// down to 2^-16 of the largest. Scores enter P V, S enters Q S and the decayed K
-// enters S with as many terms as the operands have: in bf16 calls each is one
-// rounding, of the kind that brought K itself to bf16, and with the output's own
-// (1.66e-3 of the result) the error is 2.4e-3. A second term of the decayed K
-// makes that 2.3e-3 and costs 8 % (32 x 1024 rows 29.8 us against 27.2, gradients
-// of 8 x 4096 167 against 153). Where the state is an output, which is fp32, the
-// decayed K has three terms. The tensor pipe cuts its fp32 sums off instead of
-// rounding them, which is a bias: with three terms each block's products are
-// summed apart and added to the state by an ordinary, rounded fma.
+// down to 2^-16 of the largest. What is computed on the way into a product (a
+// weighted score into P V, S into Q S, the decayed K into S) is two bf16 terms in
+// bf16 calls, within 2^-16, and three in fp32 ones. A bf16 result is then
+// rounded once, at the end: its error is that rounding's own, 1.66e-3 of the
+// result. With one term each it was 2.4e-3, and 27.2 us instead of 33.3 for
+// 32 x 1024 rows, 148 instead of 190 for the gradients of 8 x 4096. Where the
+// state is an output, which is fp32, the decayed K has three terms. The tensor
+// pipe cuts its fp32 sums off instead of rounding them, which is a bias: with
+// three terms each block's products are summed apart and added to the state by
+// an ordinary, rounded fma.
 
 constexpr int BLK = 64;        // rows of a block
 constexpr int CH_THREADS = 128;  // of the segments' own states
@@ -192,8 +193,10 @@ struct Tile {
 };
 // The state as an operand: HD rows in the same arrangement.
 
+// Terms of an operand that the call is given (N) and of one that is computed on the way, a weighted score or the
+// state (MID)
 template <typename T>
-struct Terms { static constexpr int N = sizeof(T) == 2 ? 1 : 3; };
+struct Terms { static constexpr int N = sizeof(T) == 2 ? 1 : 3, MID = sizeof(T) == 2 ? 2 : 3; };
 
 // fp32 tiles: n rows (zeros up to 64) of a head's columns, from src on, through
 // registers into the three planes of a tile. A thread takes one 16-byte column
@@ -743,11 +746,12 @@ template <typename T, int HD, bool BACK>
 struct PassShape {
   static constexpr int NT = Terms<T>::N, TILES = BACK ? 4 : 3, WARPS = BACK ? 12 : 8, THREADS = WARPS * 32;
   static constexpr int STAGES = NT == 1 ? 3 : 1;  // tiles in flight; fp32 splits its tiles on the way in
+  static constexpr int STATES = NT == 1 ? 2 : 1;  // operand planes of the state: the step's and the next one's
 };
 template <typename T, int HD, bool BACK>
 __host__ __device__ constexpr int pass_smem() {
   using Q = PassShape<T, HD, BACK>;
-  return Q::STAGES * (Q::TILES * Q::NT * Tile<HD>::BYTES + Q::NT * HD * HD * 2);
+  return Q::STAGES * Q::TILES * Q::NT * Tile<HD>::BYTES + Q::STATES * Terms<T>::MID * HD * HD * 2;
 }
 
 // Of a block's rows: exponents from the row before the block; the decay between
@@ -767,7 +771,7 @@ __device__ __forceinline__ void block_output(float (&o)[HD / 8][4], const Frag<H
                                              const float* wt, int warp, int lane, int rows, float scale) {
   using L = Tile<HD>;
   constexpr bool FINE = Terms<T>::N == 3;
-  constexpr int NT = Terms<T>::N, ST = HD * HD * 2, N = HD / 16, QN = NT == 1 ? N : 1;
+  constexpr int NT = Terms<T>::N, MT = Terms<T>::MID, ST = HD * HD * 2, N = HD / 16, QN = NT == 1 ? N : 1;
   const int i0 = warp * 16 + (lane >> 2);
   const float2 ei0 = e[i0], ei1 = e[i0 + 8];
   uint32_t qf[QN][NT][4];  // bf16 keeps its own rows' fragments, fp32 reads them again
@@ -785,12 +789,9 @@ __device__ __forceinline__ void block_output(float (&o)[HD / 8][4], const Frag<H
 #pragma unroll
     for (int t = 0; t < NT; ++t) f.bt(vb[g % QN][t], tw + t * L::BYTES, kb * 16, g);
   };
-  auto read_state = [&](int kk, int g) {  // into vb
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      if (STATE_T) f.b(vb[g % QN][t], state + t * ST, g * 16, kk);
-      else f.bt(vb[g % QN][t], state + t * ST, kk * 16, g);
-    }
+  auto read_state = [&](uint32_t (&r)[4], int kk, int g, int t) {
+    if (STATE_T) f.b(r, state + t * ST, g * 16, kk);
+    else f.bt(r, state + t * ST, kk * 16, g);
   };
   if (NT == 1)
 #pragma unroll
@@ -798,19 +799,35 @@ __device__ __forceinline__ void block_output(float (&o)[HD / 8][4], const Frag<H
   if (!has_state) {
 #pragma unroll
     for (int n = 0; n < HD / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
-  } else {
-    if (NT == 1)
+  } else if (NT == 1) {
+    // the state's small terms first, then its large ones
 #pragma unroll
-      for (int g = 0; g < N; ++g) read_state(0, g);
+    for (int g = 0; g < N; ++g) read_state(vb[g % QN][0], 0, g, MT - 1);
 #pragma unroll
-    for (int kk = 0; kk < N; ++kk) {
-      if (NT > 1) read_own(kk);
+    for (int i = 0; i < MT * N; ++i) {
+      const int kk = i % N, next = i + 1;
 #pragma unroll
       for (int g = 0; g < N; ++g) {
-        if (NT > 1) read_state(kk, g);
-        if (kk == 0) mma_terms<NT, true>(o[2 * g], o[2 * g + 1], qf[kk % QN], vb[g % QN]);
-        else mma_terms<NT>(o[2 * g], o[2 * g + 1], qf[kk % QN], vb[g % QN]);
-        if (NT == 1 && kk + 1 < N) read_state(kk + 1, g);
+        if (i == 0) {
+          mma16816_new(o[2 * g], qf[kk % QN][0], vb[g % QN][0][0], vb[g % QN][0][1]);
+          mma16816_new(o[2 * g + 1], qf[kk % QN][0], vb[g % QN][0][2], vb[g % QN][0][3]);
+        } else {
+          mma16816(o[2 * g], qf[kk % QN][0], vb[g % QN][0][0], vb[g % QN][0][1]);
+          mma16816(o[2 * g + 1], qf[kk % QN][0], vb[g % QN][0][2], vb[g % QN][0][3]);
+        }
+        if (next < MT * N) read_state(vb[g % QN][0], next % N, g, MT - 1 - next / N);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int kk = 0; kk < N; ++kk) {
+      read_own(kk);
+#pragma unroll
+      for (int g = 0; g < N; ++g) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) read_state(vb[0][t], kk, g, t);
+        if (kk == 0) mma_terms<NT, true>(o[2 * g], o[2 * g + 1], qf[0], vb[0]);
+        else mma_terms<NT>(o[2 * g], o[2 * g + 1], qf[0], vb[0]);
       }
     }
   }
@@ -840,18 +857,28 @@ __device__ __forceinline__ void block_output(float (&o)[HD / 8][4], const Frag<H
     }
   };
   auto values = [&](const float (&s)[2][4], int kb) {
-    uint32_t pa[NT][4];
+    uint32_t pa[MT][4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {  // the accumulators are the next product's A fragment
-      uint32_t t[NT];
-      terms2<NT>(s[r >> 1][(r & 1) * 2], s[r >> 1][(r & 1) * 2 + 1], t);
+      uint32_t t[MT];
+      terms2<MT>(s[r >> 1][(r & 1) * 2], s[r >> 1][(r & 1) * 2 + 1], t);
 #pragma unroll
-      for (int k = 0; k < NT; ++k) pa[k][r] = t[k];
+      for (int k = 0; k < MT; ++k) pa[k][r] = t[k];
     }
+    if (NT == 1) {
 #pragma unroll
-    for (int g = 0; g < N; ++g) {
-      if (NT > 1) read_values(kb, g);
-      mma_terms<NT>(o[2 * g], o[2 * g + 1], pa, vb[g % QN]);
+      for (int t = MT - 1; t >= 0; --t)
+#pragma unroll
+        for (int g = 0; g < N; ++g) {
+          mma16816(o[2 * g], pa[t], vb[g % QN][0][0], vb[g % QN][0][1]);
+          mma16816(o[2 * g + 1], pa[t], vb[g % QN][0][2], vb[g % QN][0][3]);
+        }
+    } else {
+#pragma unroll
+      for (int g = 0; g < N; ++g) {
+        read_values(kb, g);
+        mma_terms<NT>(o[2 * g], o[2 * g + 1], pa, vb[0]);
+      }
     }
   };
   // the 16 x 16 blocks, the diagonal one first; then wholly on one side
@@ -933,7 +960,7 @@ __global__ void __launch_bounds__(PassShape<T, HD, BACK>::THREADS, pass_blocks<T
   using L = Tile<HD>;
   using P = StatePart<HD>;
   constexpr int NT = Q::NT, PLANE = NT * L::BYTES, STAGE = Q::TILES * PLANE, STAGES = Q::STAGES;
-  constexpr int ST = HD * HD * 2, SPLANE = NT * ST, DECS = NT == 1 ? STAGES : 2;
+  constexpr int MT = Terms<T>::MID, SPLANE = MT * HD * HD * 2, DECS = NT == 1 ? STAGES : 2;
   constexpr int OUT = BACK ? 8 : 4;  // warps OUT .. OUT + 3 have the state
   constexpr int LOADER = (OUT + 3) * 32;
   extern __shared__ __align__(1024) char smem[];
@@ -1087,7 +1114,7 @@ __global__ void __launch_bounds__(PassShape<T, HD, BACK>::THREADS, pass_blocks<T
         const float2 y = *reinterpret_cast<const float2*>(src + 8 * HD + n * 8);
         S[n][0] = x.x; S[n][1] = x.y; S[n][2] = y.x; S[n][3] = y.y;
       }
-      put_state<HD, NT>(sbase, S, sw, lane);
+      put_state<HD, MT>(sbase, S, sw, lane);
     }
     if (NT == 1) arrive(ready, 0);
     // x by its columns that are this warp's rows of the state, y by the state's columns
@@ -1110,8 +1137,8 @@ __global__ void __launch_bounds__(PassShape<T, HD, BACK>::THREADS, pass_blocks<T
       }
       if (NT == 1) {
         if (more) {
-          if (s + 1 >= STAGES) wait(done, s + 1 - STAGES);  // the buffers of the step that had them before
-          if (on) put_state<HD, NT>(sbase + ((s + 1) % STAGES) * SPLANE, S, sw, lane);
+          if (s > 0) wait(done, s - 1);  // the state's buffer of the step before, and the decays' of the one before that
+          if (on) put_state<HD, MT>(sbase + ((s + 1) % Q::STATES) * SPLANE, S, sw, lane);
           put_decays(s + 1);
           arrive(ready, s + 1);
           read_times(s + 2);
@@ -1121,7 +1148,7 @@ __global__ void __launch_bounds__(PassShape<T, HD, BACK>::THREADS, pass_blocks<T
         put_decays(s + 1);
         read_times(s + 2);
         finish(s);
-        if (more && on) put_state<HD, NT>(sbase, S, sw, lane);
+        if (more && on) put_state<HD, MT>(sbase, S, sw, lane);
       }
     }
     if (STAGES > 1 && tid == LOADER && stopped()) drain<STAGES>(full, issued);
@@ -1143,7 +1170,7 @@ __global__ void __launch_bounds__(PassShape<T, HD, BACK>::THREADS, pass_blocks<T
     begin(s);
     const int c = block_of(s), rows = min(BLK, it.rows - c * BLK);
     const uint32_t t0 = base + (s % STAGES) * STAGE, t1 = t0 + PLANE, t2 = t1 + PLANE, t3 = t2 + PLANE;
-    const uint32_t ts = sbase + (s % STAGES) * SPLANE;
+    const uint32_t ts = sbase + (s % Q::STATES) * SPLANE;
     const float2* e = dec.e[s % DECS];
     const float* wt = dec.w[s % DECS];
     const bool has_state = starts || s > 0;
@@ -1418,24 +1445,24 @@ cudaError_t join_hd(bool back, int n_users, const DecayArgs& a, cudaStream_t s) 
                   dim3(JOIN_THREADS), 0, s, a);
 }
 
-// Three terms of the decayed K (KT) only where the state is an output
+// Terms of the decayed K (KT): three where the state is an output, else as many as Terms::MID
 template <int HD>
 cudaError_t part_any(bool bf, bool back, bool exact, const DecayArgs& a, const void* x0, const void* y0,
                      const void* x1, const void* y1, cudaStream_t s) {
   if (!bf) return part_hd<float, HD, 3>(back, a, x0, y0, x1, y1, s);
-  return exact ? part_hd<bf16, HD, 3>(back, a, x0, y0, x1, y1, s) : part_hd<bf16, HD, 1>(back, a, x0, y0, x1, y1, s);
+  return exact ? part_hd<bf16, HD, 3>(back, a, x0, y0, x1, y1, s) : part_hd<bf16, HD, 2>(back, a, x0, y0, x1, y1, s);
 }
 template <int HD>
 cudaError_t pass_any(bool bf, bool exact, int n, const DecayArgs& a, const void* q, const void* k, const void* v,
                      void* o, cudaStream_t s) {
   if (!bf) return pass_hd<float, HD, 3, false>(n, a, q, k, v, nullptr, o, nullptr, s);
   return exact ? pass_hd<bf16, HD, 3, false>(n, a, q, k, v, nullptr, o, nullptr, s)
-               : pass_hd<bf16, HD, 1, false>(n, a, q, k, v, nullptr, o, nullptr, s);
+               : pass_hd<bf16, HD, 2, false>(n, a, q, k, v, nullptr, o, nullptr, s);
 }
 template <int HD>
 cudaError_t dkdv_any(bool bf, int n, const DecayArgs& a, const void* q, const void* k, const void* v, const void* g,
                      void* dk, void* dv, cudaStream_t s) {
-  return bf ? pass_hd<bf16, HD, 1, true>(n, a, q, g, k, v, dk, dv, s)
+  return bf ? pass_hd<bf16, HD, 2, true>(n, a, q, g, k, v, dk, dv, s)
             : pass_hd<float, HD, 3, true>(n, a, q, g, k, v, dk, dv, s);
 }
 
