@@ -467,13 +467,14 @@ __device__ __forceinline__ float2 exponent(double decay2, long long steps) {
   const float hi = (float)x;
   return make_float2(hi, (float)(x - (double)hi));
 }
-// 2^(hi + lo) for hi + lo <= 0. The approximation is off by 2^-22, which a state
+// 2^min(hi + lo, 0): over a decrease of the timestamps the sum is positive. The approximation is off by 2^-22, which a state
 // that is an output, or fp32 rows, show after a few factors: FINE sums the
 // exponential series of the fraction (|f ln 2| <= 0.35: the eighth power's term
 // is below 2^-27) and puts the whole part into the exponent.
 template <bool FINE>
 __device__ __forceinline__ float decay_exp2(float hi, float lo) {
   if (!FINE) return exp2_approx(fminf(hi + lo, 0.f));
+  if (hi + lo >= 0.f) return 1.f;
   if (hi + lo < -126.f) return 0.f;
   const float n = rintf(hi + lo), t = ((hi - n) + lo) * 0.69314718055994531f;
   float p = 1.f / 5040;

@@ -54,3 +54,66 @@ def test_decay_bf16_results_are_rounded_once(cuda, hd, lengths):
     big = O.decay_attention_backward(q, k, v, ts, cu, taus, decay, d_o, magnitude=True)
     for name, g, r, m in zip(("dq", "dk", "dv"), R.decay_attn_backward(*t, cu, heads, ts=tts), ref, big):
         _rounded_once(g, r, m, L, hd, name)
+
+
+# ---------------------------------------------------------------- timestamps that decrease
+
+
+def _times(pattern, T):
+    """Seconds since the history's first token, which decrease somewhere."""
+    i = np.arange(T)
+    if pattern == "steps":        # whole sixteens, up and down by hundreds of buckets
+        return np.array([0, 1000, 500, 2000, 700])[i // 16 % 5]
+    raise ValueError(pattern)
+
+
+def _weights(cuda, dtype, hd, heads, cu, ts, lo, hi, others, rng_seed=1):
+    """The factor by which row j counts in row i of the history lo .. hi - 1, read
+    off every output of the calls, {name: [n_heads, n, n]} and, from the state,
+    [n_heads, n] for the last row: one-hot rows in one operand, constant ones in
+    the others, whose products are exact. The other histories have the rows
+    ``others``; what they give is returned too."""
+    H, T, n = heads.n_heads, int(cu[-1]), hi - lo
+    tts = torch.from_numpy(ts).to(cuda)
+    one = torch.zeros(n, H, hd, device=cuda)
+    one[:, :, 0] = 1.0
+    root = float(hd) ** 0.5                       # 4 or 8: exact
+    W4 = {name: torch.zeros(H, n, n, device=cuda) for name in ("o", "o with a state", "dq", "dk", "dv")}
+    left, rest = torch.zeros(H, n, device=cuda), []
+
+    def rows(x):
+        full = others.clone()
+        full[lo:hi] = x.reshape(n, H * hd).to(full.dtype)
+        return full
+
+    for b in range(0, n, hd):
+        m = min(hd, n - b)
+        hot = torch.zeros(n, H, hd, device=cuda)
+        hot[torch.arange(b, b + m), :, torch.arange(m)] = 1.0
+        state = R.DecayState(heads, len(cu) - 1, device=cuda)
+        q, k, v = rows(one * root), rows(one), rows(hot)
+        kw = dict(ts=tts, check=False)
+        o = [R.decay_attn_forward(q, k, v, cu, heads, **kw), R.decay_attn_forward(q, k, v, cu, heads, state=state, **kw)]
+        g = [R.decay_attn_backward(rows(one), rows(hot), rows(one), rows(one * root), cu, heads, **kw),
+             R.decay_attn_backward(rows(hot), rows(one), rows(one), rows(one * root), cu, heads, **kw),
+             R.decay_attn_backward(rows(one * root), rows(one), rows(one), rows(hot), cu, heads, **kw)]
+        for name, x in (("o", o[0]), ("o with a state", o[1]), ("dq", g[0][0])):
+            W4[name][:, :, b:b + m] = x[lo:hi].float().view(n, H, hd).permute(1, 0, 2)[:, :, :m]
+        for name, x in (("dk", g[1][1]), ("dv", g[2][2])):
+            W4[name][:, b:b + m, :] = x[lo:hi].float().view(n, H, hd).permute(1, 2, 0)[:, :m, :]
+        u = [int(x) for x in cu].index(lo)
+        left[:, b:b + m] = state.s[u, :, 0, :m]
+        rest += [x[r] for x in (*o, *g[0]) for r in (slice(0, lo), slice(hi, T))]
+        rest += [state.s[w] for w in range(len(cu) - 1) if w != u]
+    return {name: w.cpu().numpy().astype(np.float64) for name, w in W4.items()}, left.cpu().numpy().astype(np.float64), rest
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_decay_weights_over_a_far_decrease(cuda, dtype):
+    """Hundreds of half-lives back: every factor stays between 0 and 1, also in the state."""
+    cu = np.array([0, 200], dtype=np.int32)
+    heads = R.DecayHeads((1, 60), (-0.7, -0.9), 16)
+    ts = 10 ** 9 + _times("steps", 200).astype(np.int64)
+    got, left, _ = _weights(cuda, dtype, 16, heads, cu, ts, 0, 200, torch.zeros(200, 32, device=cuda, dtype=DT[dtype]))
+    for name, w in {**got, "state": left}.items():
+        assert np.all((w >= 0) & (w <= 1 + 64 * U32 + U16)), name
