@@ -405,9 +405,12 @@ rest_status rest_embed_backward(rest_dtype dt, long long n_rows, int d, const vo
  * (rotated queries and keys, gated values). n_i - n_{i-1} is exact (int64).
  *
  * log_decay: host [n_heads], g_h in -10000 .. 0 (0 keeps everything).
- * ts: dev [T] int64 seconds, non-decreasing within each user (a decrease sets
- * *dev_err = REST_ERR_UNSORTED_TIME and counts as no time passing); may be
- * NULL when every tau_h is 0.
+ * ts: dev [T] int64 seconds, non-decreasing within each user; may be NULL when
+ * every tau_h is 0. A decrease sets *dev_err = REST_ERR_UNSORTED_TIME. Rows on
+ * one side of it then weigh one another as defined all the same (indexes of
+ * timestamps before the history's first are negative), rows on both sides by
+ * some number from 0 to 1 in place of exp(g_h (n_i - n_j)), and other histories
+ * are not concerned.
  *
  * T is below 2^30 (REST_ERR_UNSUPPORTED beyond). Outputs overlap no input. A
  * value that is not finite stays in its history: it reaches the rows that
@@ -463,8 +466,8 @@ rest_status rest_decay_attn_backward(rest_dtype dt, const rest_heads* heads, con
  * everything else stay as they were. Any other slot outside 0 .. n_slots-1,
  * or one that an earlier entry of the call has, is skipped the same way and
  * sets *dev_err = REST_ERR_INVALID_ARG. A timestamp before the slot's last one
- * sets REST_ERR_UNSORTED_TIME and counts as no time passing. Needs no
- * workspace; n is at most 65535. */
+ * sets REST_ERR_UNSORTED_TIME and counts as no time passing (what follows counts
+ * from it). Needs no workspace; n is at most 65535. */
 rest_status rest_decay_attn_step(rest_dtype dt, const rest_heads* heads, const double* log_decay, int n,
                                  const void* q, const void* k, const void* v, const int64_t* ts,
                                  const rest_decay_state* state, const int32_t* slots, void* o, int32_t* dev_err,

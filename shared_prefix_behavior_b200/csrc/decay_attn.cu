@@ -10,9 +10,16 @@
 namespace rest {
 namespace {
 
-// Rotation index of a head: token count for a position head, whole buckets of
-// tau seconds since the history's first token for a time head.
-__device__ __forceinline__ long long buckets(long long dt, long long tau) { return dt > 0 ? dt / tau : 0; }
+// Rotation index of a time head: whole buckets of tau seconds, dt seconds after
+// the history's first token (rounded down before it, where only timestamps that
+// decrease lead). inv = 1 / tau.
+__device__ __forceinline__ long long buckets(long long dt, long long tau, double inv) {
+  long long n;
+  if (dt >= (1LL << 52) || dt <= -(1LL << 52)) n = dt / tau;
+  else n = (long long)((double)dt * inv);  // within one of the quotient: both are below 2^52
+  const long long r = dt - n * tau;
+  return r < 0 ? n - 1 : r >= tau ? n + 1 : n;
+}
 
 // ---------------------------------------------------------------- prologue
 
@@ -436,15 +443,7 @@ struct Index {
   double inv;
   int row0;
   const int64_t* ts;
-  __device__ long long of_time(long long t) const {
-    const long long dt = t - t0;
-    if (dt <= 0) return 0;
-    if (dt >= (1LL << 52)) return dt / tau;
-    // the product is within one of the quotient: both are below 2^52
-    long long n = (long long)((double)dt * inv);
-    const long long r = dt - n * tau;
-    return r < 0 ? n - 1 : r >= tau ? n + 1 : n;
-  }
+  __device__ long long of_time(long long t) const { return buckets(t - t0, tau, inv); }
   // of the history's last cached row; without one, of its first row
   __device__ long long before(const DecayRec& rec) const {
     return tau > 0 ? of_time(rec.tprev) : rec.len0 > 0 ? rec.len0 - 1 : 0;
@@ -461,9 +460,10 @@ __device__ __forceinline__ Index head_index(const DecayArgs& a, const DecayRec& 
   x.ts = a.ts;
   return x;
 }
-// decay2 * steps (<= 0; steps below zero, after a decrease of the timestamps, count as none) as two floats
+// decay2 * steps as two floats (positive where the timestamps decrease on the way: what becomes of two such
+// exponents' difference is clamped, not they, so that rows on one side of a decrease keep their distance)
 __device__ __forceinline__ float2 exponent(double decay2, long long steps) {
-  const double x = decay2 * (double)(steps > 0 ? steps : 0);
+  const double x = decay2 * (double)steps;
   const float hi = (float)x;
   return make_float2(hi, (float)(x - (double)hi));
 }
@@ -761,6 +761,7 @@ __host__ __device__ constexpr int pass_smem() {
 struct BlockDecays {
   float2 e[3][BLK];
   float w[3][BLK], u[3][BLK];
+  bool quotient[3][BLK / 16];  // the decays between the rows of a 16 are quotients of their w
 };
 
 // 16 own rows against the block's rows before (BACK: after) them and the state.
@@ -769,7 +770,8 @@ struct BlockDecays {
 template <typename T, int HD, bool BACK, bool STATE_T>
 __device__ __forceinline__ void block_output(float (&o)[HD / 8][4], const Frag<HD>& f, uint32_t ta, uint32_t tb,
                                              uint32_t tw, uint32_t state, bool has_state, const float2* e,
-                                             const float* wt, int warp, int lane, int rows, float scale) {
+                                             const float* wt, const bool* quotient, int warp, int lane, int rows,
+                                             float scale) {
   using L = Tile<HD>;
   constexpr bool FINE = Terms<T>::N == 3;
   constexpr int NT = Terms<T>::N, MT = Terms<T>::MID, ST = HD * HD * 2, N = HD / 16, QN = NT == 1 ? N : 1;
@@ -893,10 +895,8 @@ __device__ __forceinline__ void block_output(float (&o)[HD / 8][4], const Frag<H
 #pragma unroll
       for (int kk = 0; kk < N; ++kk) read_keys(first, kk);
     auto in = [&](int own, int other) { return BACK ? other >= own : other <= own; };
-    // Within the 16 rows D is the quotient of the decays to (BACK: from) their end,
-    // while that of all 16 is far from the smallest number.
-    const bool quotient = wt[BACK ? warp * 16 + 15 : warp * 16] >= 0x1p-60f;
-    if (quotient) {
+    // Within the 16 rows D is the quotient of the decays to (BACK: from) their end
+    if (quotient[warp]) {
       const float x0 = scale / wt[i0], x1 = scale / wt[i0 + 8];
       const float2 w0 = *reinterpret_cast<const float2*>(&wt[j]), w1 = *reinterpret_cast<const float2*>(&wt[j + 8]);
       s[0][0] *= x0 * w0.x; s[0][1] *= x0 * w0.y; s[0][2] *= x1 * w0.x; s[0][3] *= x1 * w0.y;
@@ -1095,7 +1095,13 @@ __global__ void __launch_bounds__(PassShape<T, HD, BACK>::THREADS, pass_blocks<T
       dec.e[s % DECS][st] = e;
       const int end = BACK ? lane & 16 : lane | 15;
       const float2 x = make_float2(__shfl_sync(0xffffffffu, e.x, end), __shfl_sync(0xffffffffu, e.y, end));
-      dec.w[s % DECS][st] = BACK ? decay_between<NT == 3>(e, x) : decay_between<NT == 3>(x, e);
+      const float w = BACK ? decay_between<NT == 3>(e, x) : decay_between<NT == 3>(x, e);
+      dec.w[s % DECS][st] = w;
+      // while they are far from the smallest number and no timestamp decreases between the rows, which
+      // their clamped decays would not show
+      const long long before = __shfl_up_sync(0xffffffffu, n, 1);
+      const uint32_t good = __ballot_sync(0xffffffffu, w >= 0x1p-60f && ((lane & 15) == 0 || n >= before));
+      if ((lane & 15) == 0) dec.quotient[s % DECS][st >> 4] = ((good >> lane) & 0xffffu) == 0xffffu;
       dec.u[s % DECS][st] = BACK ? decay_exp2<KT == 3>(e.x, e.y) : decay_between<KT == 3>(exponent(decay2, n_end), e);
     };
     read_times(0);
@@ -1174,18 +1180,19 @@ __global__ void __launch_bounds__(PassShape<T, HD, BACK>::THREADS, pass_blocks<T
     const uint32_t ts = sbase + (s % Q::STATES) * SPLANE;
     const float2* e = dec.e[s % DECS];
     const float* wt = dec.w[s % DECS];
+    const bool* quotient = dec.quotient[s % DECS];
     const bool has_state = starts || s > 0;
     if (w * 16 < rows) {
       float o[HD / 8][4];
       const size_t at = off + (size_t)c * BLK * d;
       if (!BACK) {
-        block_output<T, HD, false, false>(o, f, t0, t1, t2, ts, has_state, e, wt, w, lane, rows, a.scale);
+        block_output<T, HD, false, false>(o, f, t0, t1, t2, ts, has_state, e, wt, quotient, w, lane, rows, a.scale);
         store_rows<T, HD>(out0 + at, d, t0, o, rows, w, lane);
       } else if (warp < 4) {  // dV from K, Q, dO and G; the rows of K are no other warp's
-        block_output<T, HD, true, false>(o, f, t2, t0, t1, ts, has_state, e, wt, w, lane, rows, a.scale);
+        block_output<T, HD, true, false>(o, f, t2, t0, t1, ts, has_state, e, wt, quotient, w, lane, rows, a.scale);
         store_rows<T, HD>(out1 + at, d, t2, o, rows, w, lane);
       } else {                // dK from V, dO, Q and G^T
-        block_output<T, HD, true, true>(o, f, t3, t1, t0, ts, has_state, e, wt, w, lane, rows, a.scale);
+        block_output<T, HD, true, true>(o, f, t3, t1, t0, ts, has_state, e, wt, quotient, w, lane, rows, a.scale);
         store_rows<T, HD>(out0 + at, d, t3, o, rows, w, lane);
       }
     }
@@ -1257,7 +1264,7 @@ __global__ void __launch_bounds__(STEP_THREADS, 4) decay_step_kernel(DecayHeadsA
   if (in && tid < H) {
     const long long tau = hs.tau[tid];
     long long n = 1;
-    if (tau > 0) n = max(0LL, buckets(t - t_first, tau) - buckets(t_last - t_first, tau));
+    if (tau > 0) n = max(0LL, buckets(t - t_first, tau, hs.inv[tid]) - buckets(t_last - t_first, tau, hs.inv[tid]));
     keep[tid] = (float)exp2(hs.decay2[tid] * (double)n);
   }
   int bad = slot < -1 || slot >= st.n_slots;

@@ -59,12 +59,45 @@ def test_decay_bf16_results_are_rounded_once(cuda, hd, lengths):
 # ---------------------------------------------------------------- timestamps that decrease
 
 
+def test_decay_step_counts_a_decrease_as_no_time(cuda):
+    """Factor 1 over the decrease, also to a time before the history's first; what follows counts from there."""
+    heads = R.DecayHeads((1, 60), (-0.01, -0.5), 16)
+    state = R.DecayState(heads, 1, device=cuda)
+    hot = torch.zeros(5, 2, 16, device=cuda)
+    hot[torch.arange(5), :, torch.arange(5)] = 1.0
+    one = torch.zeros(1, 2, 16, device=cuda)
+    one[:, :, 0] = 1.0
+    err, seen = torch.zeros(1, dtype=torch.int32, device=cuda), []
+    ts = [1000, 2000, 1500, 900, 1025]
+    for i, t in enumerate(ts):
+        R.decay_attn_step(one.view(1, 32), one.view(1, 32), hot[i:i + 1].view(1, 32), state, check=False, err=err,
+                          ts=torch.tensor([t], device=cuda))
+        seen.append(int(err))
+    assert seen == [0, 0, 2, 2, 0] and state.t_last.item() == 1025 and state.t_first.item() == 1000
+    for h, (tau, g) in enumerate(((1, -0.01), (60, -0.5))):
+        n = [(t - 1000) // tau for t in ts]
+        gaps = [max(0, b - a) for a, b in zip(n, n[1:])]
+        for j in range(5):
+            want = np.exp(g * sum(gaps[j:]))
+            assert abs(float(state.s[0, h, 0, j]) - want) <= 8 * U32 * want
+
+
 def _times(pattern, T):
     """Seconds since the history's first token, which decrease somewhere."""
     i = np.arange(T)
     if pattern == "steps":        # whole sixteens, up and down by hundreds of buckets
         return np.array([0, 1000, 500, 2000, 700])[i // 16 % 5]
-    raise ValueError(pattern)
+    if pattern == "inside":       # within every sixteen, its last row the latest
+        return np.array([0, 0, 0, 1000] + [10] * 11 + [1000])[i % 16]
+    if pattern == "far inside":   # its first row further from its last than a middle one's decay can say
+        return np.array([75] * 4 + [0] * 4 + [130] * 8)[i % 16]
+    if pattern == "blocks":       # at the 64th row
+        return 30 * (i % 64) + i // 64
+    if pattern == "below":        # before the first token, by buckets and parts of them
+        return np.where(i < 20, 7 * i, 5 * i - 1234)
+    if pattern == "years":
+        return np.where(i % 50 == 25, 10 ** 9, 100 * (i // 50)) + i
+    return np.random.default_rng(5).integers(0, 3000, T)
 
 
 def _weights(cuda, dtype, hd, heads, cu, ts, lo, hi, others, rng_seed=1):
@@ -117,3 +150,43 @@ def test_decay_weights_over_a_far_decrease(cuda, dtype):
     got, left, _ = _weights(cuda, dtype, 16, heads, cu, ts, 0, 200, torch.zeros(200, 32, device=cuda, dtype=DT[dtype]))
     for name, w in {**got, "state": left}.items():
         assert np.all((w >= 0) & (w <= 1 + 64 * U32 + U16)), name
+
+
+@pytest.mark.parametrize("pattern", ["steps", "inside", "far inside", "blocks", "below", "years", "random"])
+@pytest.mark.parametrize("dtype,hd", [("f32", 64), ("f32", 16), ("bf16", 64), ("bf16", 16)])
+def test_decay_weights_where_timestamps_decrease(cuda, dtype, hd, pattern):
+    """Two rows without a decrease between them weigh one another as defined, two
+    on both sides of one by a number from 0 to 1, later rows not at all by earlier
+    ones (exactly), and the other histories' bits do not change. A weight is a
+    product of at most five factors and 1: 64 u32 of it, and a step of the output
+    and the two-term operands in bf16 calls."""
+    lengths, taus = (40, 200, 70), (0, 1, 60, 1)
+    decay = (-0.01, -float(np.log(2.0)), -0.05, -0.01)
+    cu = np.concatenate([[0], np.cumsum(lengths)]).astype(np.int32)
+    heads, T = R.DecayHeads(taus, decay, hd), int(cu[-1])
+    rng = np.random.default_rng(3)
+    others = torch.from_numpy(rng.standard_normal((T, 4 * hd))).to(cuda, DT[dtype])
+    ts = np.concatenate([W.draw_timestamps(rng, n) for n in lengths])
+    t = _times(pattern, 200).astype(np.int64)
+    _, _, plain = _weights(cuda, dtype, hd, heads, cu, ts, 40, 240, others)
+    ts[40:240] = 10 ** 9 + t
+    got, left, rest = _weights(cuda, dtype, hd, heads, cu, ts, 40, 240, others)
+    assert all(torch.equal(a, b) for a, b in zip(rest, plain))
+    with pytest.raises(R.RestError) as e:
+        R.decay_attn_forward(others, others, others, cu, heads, ts=torch.from_numpy(ts).to(cuda))
+    assert e.value.status == 2
+    drops = np.concatenate([[0], np.cumsum(np.diff(t) < 0)])
+    i = np.arange(200)
+    for h, (tau, g) in enumerate(zip(taus, decay)):
+        n = i if tau == 0 else (t - t[0]) // tau
+        known = (drops[:, None] == drops[None, :]) | (tau == 0)
+        want = np.exp(np.minimum(g * (n[:, None] - n[None, :]), 0.0))
+        tol = 64 * U32 + (U16 + 1.02 * 2 * 2.0 ** -16 if dtype == "bf16" else 0.0)
+        low = i[:, None] >= i[None, :]
+        for name, w in got.items():
+            assert np.all(w[h][~low] == 0), (name, h)
+            assert np.all(np.abs(w[h] - want)[low & known] <= tol * want[low & known] + 2.0 ** -120), (name, h)
+            assert np.all((w[h][low] >= 0) & (w[h][low] <= 1 + tol)), (name, h)
+        last = known[-1]
+        assert np.all(np.abs(left[h] - want[-1])[last] <= 64 * U32 * want[-1][last] + 2.0 ** -120), h
+        assert np.all((left[h] >= 0) & (left[h] <= 1 + 64 * U32)), h
