@@ -248,7 +248,8 @@ def _err_word(device, stream=None):
     key = (dev, _stream(stream))
     w = _ERR_WORDS.get(key)
     if w is None:
-        w = _ERR_WORDS[key] = torch.zeros(1, dtype=torch.int32, device=dev)
+        with torch.cuda.stream(stream):  # zeroed before the call's kernels, not beside them
+            w = _ERR_WORDS[key] = torch.zeros(1, dtype=torch.int32, device=dev)
     return w
 
 
@@ -532,7 +533,11 @@ def attn_backward(q, k, v, o, o_lo, lse, d_o, cu_seqlens, n_heads: int, dq=None,
 # read the status word back and raise what a kernel reported, which
 # synchronizes; with ``check=False`` nothing synchronizes, the call can be
 # captured into a CUDA graph, and ``err`` (an int32 tensor of one element)
-# receives the status if it is given.
+# receives the status if it is given. What a call allocates (outputs and
+# workspace that are not given) is ``stream``'s memory: the caching allocator
+# hands a freed block out again at once for the stream that it was allocated on,
+# whose earlier kernels ``stream`` does not wait for. Outputs are kept for the
+# current stream's use too.
 
 
 def _expect(name: str, t, dtype, shape, device) -> None:
@@ -554,21 +559,36 @@ def _expect_ws(ws, device) -> None:
         raise ValueError("ws must be contiguous")
 
 
-def _run(fn, device, stream, check: bool, err, temporaries, *args) -> None:
-    """fn(*args, err pointer, stream handle) with ``device`` current. Tensors
-    allocated for the call alone are kept for ``stream`` if it is not the one
-    they were allocated on."""
+def _new(stream, shape, dtype, device, output: bool = True):
+    """An uninitialised tensor for a call on ``stream``."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if output:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
+def _new_ws(stream, nbytes: int, device):
+    import torch
+    return _new(stream, max(nbytes, 256), torch.uint8, device, output=False)
+
+
+def _run(fn, device, stream, check: bool, err, *args) -> None:
+    """fn(*args, err pointer, stream handle) with ``device`` current."""
     import torch
     if device.index != torch._C._cuda_getDevice():
         with torch.cuda.device(device):
-            return _run(fn, device, stream, check, err, temporaries, *args)
+            return _run(fn, device, stream, check, err, *args)
     if stream is None:
         # the handle alone: building the Stream object around it takes 3 us, about as long as the launch
         handle = torch._C._cuda_getCurrentRawStream(device.index)
+    elif stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, expected {device}")
     else:
         handle = stream.cuda_stream
-        for t in temporaries:
-            t.record_stream(stream)
     if not check:
         if err is None:
             _check(fn(*args, None, handle), fn.__name__)
@@ -605,13 +625,11 @@ def embed_forward(table, ids, scale: float = 1.0, out=None, stream=None, check=T
     if not table.is_contiguous():
         raise ValueError("table must be contiguous")
     _expect("ids", ids, torch.int64, (T,), dev)
-    made = ()
     if out is None:
-        out = torch.empty((T, d), dtype=table.dtype, device=dev)
-        made = (out,)
+        out = _new(stream, (T, d), table.dtype, dev)
     else:
         _expect("out", out, table.dtype, (T, d), dev)
-    _run(_lib.rest_embed_forward, dev, stream, check, err, made, dt, n_rows, d, table.data_ptr(), T, ids.data_ptr(),
+    _run(_lib.rest_embed_forward, dev, stream, check, err, dt, n_rows, d, table.data_ptr(), T, ids.data_ptr(),
          scale, out.data_ptr())
     return out
 
@@ -632,20 +650,17 @@ def embed_backward(d_out, ids, n_rows: int, scale: float = 1.0, d_table=None, ac
     dt = _dtype_code(d_out)
     _expect("d_out", d_out, d_out.dtype, (T, d), dev)
     _expect("ids", ids, torch.int64, (T,), dev)
-    made = []
     if d_table is None:
         if accumulate:
             raise ValueError("accumulate adds to d_table, which is not given")
-        d_table = torch.empty((n_rows, d), dtype=torch.float32, device=dev)
-        made.append(d_table)
+        d_table = _new(stream, (n_rows, d), torch.float32, dev)
     else:
         _expect("d_table", d_table, torch.float32, (n_rows, d), dev)
     if ws is None:
-        ws = _workspace(embed_workspace_size(n_rows, d, T), dev)
-        made.append(ws)
+        ws = _new_ws(stream, embed_workspace_size(n_rows, d, T), dev)
     else:
         _expect_ws(ws, dev)
-    _run(_lib.rest_embed_backward, dev, stream, check, err, made, dt, n_rows, d, d_out.data_ptr(), T, ids.data_ptr(),
+    _run(_lib.rest_embed_backward, dev, stream, check, err, dt, n_rows, d, d_out.data_ptr(), T, ids.data_ptr(),
          scale, 1 if accumulate else 0, d_table.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
     return d_table
 
@@ -754,18 +769,15 @@ def decay_attn_forward(q, k, v, cu_seqlens, heads: DecayHeads, ts=None, state: O
     dev, dt = _decay_inputs(T, heads, q, k, v, ts)
     cu, batch = _packed_batch(cu_seqlens, T)
     st, sl = _decay_slots(len(cu) - 1, state, slots, heads, dev)
-    made = []
     if o is None:
-        o = torch.empty_like(q)
-        made.append(o)
+        o = _new(stream, q.shape, q.dtype, dev)
     else:
         _expect("o", o, q.dtype, q.shape, dev)
     if ws is None:
-        ws = _workspace(decay_attn_workspace_size(dt, heads, cu), dev)
-        made.append(ws)
+        ws = _new_ws(stream, decay_attn_workspace_size(dt, heads, cu), dev)
     else:
         _expect_ws(ws, dev)
-    _run(_lib.rest_decay_attn_forward, dev, stream, check, err, made, dt, heads.heads, heads.decay,
+    _run(_lib.rest_decay_attn_forward, dev, stream, check, err, dt, heads.heads, heads.decay,
          ctypes.addressof(batch), q.data_ptr(),
          k.data_ptr(), v.data_ptr(), _ptr(ts), st, sl, o.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
     return o
@@ -779,20 +791,18 @@ def decay_attn_backward(q, k, v, d_o, cu_seqlens, heads: DecayHeads, ts=None, dq
     dev, dt = _decay_inputs(T, heads, q, k, v, ts)
     _expect("d_o", d_o, q.dtype, q.shape, dev)
     cu, batch = _packed_batch(cu_seqlens, T)
-    made, grads = [], []
+    grads = []
     for name, t in (("dq", dq), ("dk", dk), ("dv", dv)):
         if t is None:
-            t = torch.empty_like(q)
-            made.append(t)
+            t = _new(stream, q.shape, q.dtype, dev)
         else:
             _expect(name, t, q.dtype, q.shape, dev)
         grads.append(t)
     if ws is None:
-        ws = _workspace(decay_attn_workspace_size(dt, heads, cu), dev)
-        made.append(ws)
+        ws = _new_ws(stream, decay_attn_workspace_size(dt, heads, cu), dev)
     else:
         _expect_ws(ws, dev)
-    _run(_lib.rest_decay_attn_backward, dev, stream, check, err, made, dt, heads.heads, heads.decay,
+    _run(_lib.rest_decay_attn_backward, dev, stream, check, err, dt, heads.heads, heads.decay,
          ctypes.addressof(batch),
          q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(ts), d_o.data_ptr(), grads[0].data_ptr(), grads[1].data_ptr(),
          grads[2].data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
@@ -807,13 +817,11 @@ def decay_attn_step(q, k, v, state: DecayState, ts=None, slots=None, o=None, str
     n, heads = q.shape[0], state.heads
     dev, dt = _decay_inputs(n, heads, q, k, v, ts)
     st, sl = _decay_slots(n, state, slots, heads, dev)
-    made = ()
     if o is None:
-        o = torch.empty_like(q)
-        made = (o,)
+        o = _new(stream, q.shape, q.dtype, dev)
     else:
         _expect("o", o, q.dtype, q.shape, dev)
-    _run(_lib.rest_decay_attn_step, dev, stream, check, err, made, dt, heads.heads, heads.decay, n, q.data_ptr(),
+    _run(_lib.rest_decay_attn_step, dev, stream, check, err, dt, heads.heads, heads.decay, n, q.data_ptr(),
          k.data_ptr(), v.data_ptr(), _ptr(ts), st, sl, o.data_ptr())
     return o
 

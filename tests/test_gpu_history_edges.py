@@ -190,3 +190,82 @@ def test_decay_weights_where_timestamps_decrease(cuda, dtype, hd, pattern):
         last = known[-1]
         assert np.all(np.abs(left[h] - want[-1])[last] <= 64 * U32 * want[-1][last] + 2.0 ** -120), h
         assert np.all((left[h] >= 0) & (left[h] <= 1 + 64 * U32)), h
+
+
+# ---------------------------------------------------------------- streams
+
+
+def _calls(cuda):
+    """Every history call, with ``kw`` for the stream and what is given; by name."""
+    torch.manual_seed(0)
+    heads = R.DecayHeads((0, 64), (-0.1, -0.2), 32)
+    x = [torch.randn(300, 64, device=cuda) for _ in range(4)]
+    ts, cu = torch.arange(300, device=cuda) * 50, np.array([0, 300], dtype=np.int32)
+    ids = torch.arange(300, device=cuda) % 40
+    table = torch.randn(40, 64, device=cuda)
+
+    def step(**kw):
+        state = R.DecayState(heads, 300, device=cuda)
+        torch.cuda.synchronize()
+        return R.decay_attn_step(*x[:3], state, ts=ts, **kw)
+    return {"embed_forward": lambda **kw: R.embed_forward(table, ids, **kw),
+            "embed_backward": lambda **kw: R.embed_backward(x[0], ids, 40, **kw),
+            "decay_attn_forward": lambda **kw: R.decay_attn_forward(*x[:3], cu, heads, ts=ts, **kw),
+            "decay_attn_backward": lambda **kw: R.decay_attn_backward(*x, cu, heads, ts=ts, **kw),
+            "decay_attn_step": step}
+
+
+CALLS = ["embed_forward", "embed_backward", "decay_attn_forward", "decay_attn_backward", "decay_attn_step"]
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_a_call_allocates_on_its_stream(cuda, name, monkeypatch):
+    """Outputs, workspace and status word of a call on another stream are that
+    stream's memory: a block that the current stream has just freed may still be
+    in use there."""
+    call = _calls(cuda)[name]
+    want = call()
+    other = torch.cuda.Stream()
+    other.wait_stream(torch.cuda.current_stream())
+    seen = []
+
+    def watched(make):
+        def made(*a, **kw):
+            if str(kw.get("device", "")).startswith("cuda") or "like" in make.__name__:
+                seen.append(torch.cuda.current_stream())
+            return make(*a, **kw)
+        return made
+
+    torch.cuda.synchronize()
+    with monkeypatch.context() as m:
+        for f in ("empty", "empty_like", "zeros"):
+            m.setattr(torch, f, watched(getattr(torch, f)))
+        before = torch.cuda.current_stream()
+        got = call(stream=other)
+        assert torch.cuda.current_stream() == before
+    if name == "decay_attn_step":
+        seen = seen[4:]                       # the test's own state
+    assert len(seen) >= 2 - (name == "decay_attn_step") and all(s == other for s in seen)
+    torch.cuda.synchronize()
+    for a, b in zip(got if isinstance(got, tuple) else (got,), want if isinstance(want, tuple) else (want,)):
+        assert torch.equal(a, b)
+
+
+def test_outputs_on_another_stream_outlive_their_use_on_the_current_one(cuda):
+    """Memory of an output that the current stream still reads is not handed out again by its own stream."""
+    calls = _calls(cuda)
+    big = torch.randn(8192, 8192, device=cuda)
+    want = calls["embed_forward"]()
+    other = torch.cuda.Stream()
+    other.wait_stream(torch.cuda.current_stream())
+    out = calls["embed_forward"](stream=other, check=False)
+    torch.cuda.current_stream().wait_stream(other)
+    for _ in range(4):
+        big = big @ big                        # keeps the current stream busy
+    kept = out.clone()
+    where = out.data_ptr()
+    del out
+    again = calls["embed_forward"](stream=other, check=False)
+    assert again.data_ptr() != where
+    torch.cuda.synchronize()
+    assert torch.equal(kept, want) and torch.equal(again, want)
