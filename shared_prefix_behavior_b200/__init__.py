@@ -229,9 +229,24 @@ def workspace_size(dtype: int, taus, d: int, cu_seqlens, layers: Sequence[dict] 
     return out.value
 
 
-def _workspace(nbytes: int, device):
+def _new(stream, shape, dtype, device, output: bool = True):
+    """An uninitialised tensor for a call on ``stream``, that stream's memory:
+    the caching allocator hands a freed block out again at once for the stream
+    that it was allocated on, whose earlier kernels another stream does not wait
+    for. An output is kept for the current stream's use too."""
     import torch
-    return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if output:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
+def _workspace(nbytes: int, device, stream=None):
+    import torch
+    return _new(stream, max(nbytes, 256), torch.uint8, device, output=False)
 
 
 _ERR_WORDS = {}
@@ -268,11 +283,10 @@ def rotation_table(ts, cu_seqlens, taus, head_dim: int, rope_base: float = 10000
     H = len(taus)
     T = ts.shape[0]
     h = _Host(taus, H * head_dim, rope_base, cu_seqlens)
-    idx = torch.empty((T, H), dtype=torch.int64, device=dev)
-    cos = torch.empty((T, H, head_dim // 2), dtype=torch.float32, device=dev)
-    sin = torch.empty_like(cos)
+    idx = _new(stream, (T, H), torch.int64, dev)
+    cos, sin = (_new(stream, (T, H, head_dim // 2), torch.float32, dev) for _ in range(2))
     nb = workspace_size(REST_F32, taus, H * head_dim, cu_seqlens, rope_base=rope_base)
-    ws, err = _workspace(nb, dev), _err_word(dev, stream)
+    ws, err = _workspace(nb, dev, stream), _err_word(dev, stream)
     _check(_lib.rest_rotation_table(ctypes.byref(h.heads), ctypes.byref(h.batch), _ptr(ts), _ptr(idx), _ptr(cos),
                                     _ptr(sin), _ptr(ws), ws.numel(), _ptr(err), _stream(stream)), "rest_rotation_table")
     if check:
@@ -283,15 +297,14 @@ def rotation_table(ts, cu_seqlens, taus, head_dim: int, rope_base: float = 10000
 def encoder_attn(x, ts, cu_seqlens, taus, layers: Sequence[dict], l_switch: int, rope_base: float = 10000.0,
                  h_out=None, ws=None, stream=None, check=True):
     """Encoder T over packed histories: returns H [T, d] in x's dtype (ReST §3.2)."""
-    import torch
     dev, d = x.device, x.shape[1]
     dt = _dtype_code(x)
     h = _Host(taus, d, rope_base, cu_seqlens)
     arr = _enc_layers(layers)
     if h_out is None:
-        h_out = torch.empty_like(x)
+        h_out = _new(stream, x.shape, x.dtype, dev)
     if ws is None:
-        ws = _workspace(workspace_size(dt, taus, d, cu_seqlens, layers, rope_base=rope_base), dev)
+        ws = _workspace(workspace_size(dt, taus, d, cu_seqlens, layers, rope_base=rope_base), dev, stream)
     err = _err_word(dev, stream)
     _check(_lib.rest_encoder_attn(dt, ctypes.byref(h.heads), ctypes.byref(h.batch), _ptr(x), _ptr(ts), arr,
                                   len(layers), l_switch, _ptr(h_out), _ptr(ws), ws.numel(), _ptr(err),
@@ -317,9 +330,9 @@ def cross_decode(hmem, cu_seqlens, taus, reqs, z, dec: dict, rope_base: float = 
     h = _Host(taus, d, rope_base, cu_seqlens, reqs)
     dp = _dec(dec)
     if y_out is None:
-        y_out = torch.empty(z.shape, dtype=torch.float32, device=dev)
+        y_out = _new(stream, z.shape, torch.float32, dev)
     if ws is None:
-        ws = _workspace(workspace_size(dt, taus, d, cu_seqlens, (), reqs, dp.K, rope_base), dev)
+        ws = _workspace(workspace_size(dt, taus, d, cu_seqlens, (), reqs, dp.K, rope_base), dev, stream)
     err = _err_word(dev, stream)
     _check(_lib.rest_cross_decode(dt, ctypes.byref(h.heads), ctypes.byref(h.batch), _ptr(hmem), ctypes.byref(h.reqs),
                                   _ptr(z), ctypes.byref(dp), _ptr(y_out), _ptr(ws), ws.numel(), _ptr(err),
@@ -347,7 +360,7 @@ def cross_decode_static_ws(hmem, cu_seqlens, taus, reqs, z, dec: dict, rope_base
     h = _Host(taus, d, rope_base, cu_seqlens, reqs)
     dp = _dec(dec)
     if y_out is None:
-        y_out = torch.empty(z.shape, dtype=torch.float32, device=dev)
+        y_out = _new(stream, z.shape, torch.float32, dev)
     if err is None:
         err = _err_word(dev, stream)
     _check(_lib.rest_cross_decode_static_ws(dt, ctypes.byref(h.heads), ctypes.byref(h.batch), _ptr(hmem),
@@ -368,11 +381,11 @@ def rank_request(x, ts, cu_seqlens, taus, layers: Sequence[dict], l_switch: int,
     arr = _enc_layers(layers)
     dp = _dec(dec)
     if h_out is None:
-        h_out = torch.empty_like(x)
+        h_out = _new(stream, x.shape, x.dtype, dev)
     if y_out is None:
-        y_out = torch.empty(z.shape, dtype=torch.float32, device=dev)
+        y_out = _new(stream, z.shape, torch.float32, dev)
     if ws is None:
-        ws = _workspace(workspace_size(dt, taus, d, cu_seqlens, layers, reqs, dp.K, rope_base), dev)
+        ws = _workspace(workspace_size(dt, taus, d, cu_seqlens, layers, reqs, dp.K, rope_base), dev, stream)
     err = _err_word(dev, stream)
     _check(_lib.rest_rank_request(dt, ctypes.byref(h.heads), ctypes.byref(h.batch), _ptr(x), _ptr(ts), arr,
                                   len(layers), l_switch, ctypes.byref(h.reqs), _ptr(z), ctypes.byref(dp), _ptr(h_out),
@@ -448,15 +461,14 @@ def encoder_append(x, ts, cu_new, taus, layers: Sequence[dict], l_switch: int, c
     new rows of H [T_new, d] and writes the new keys, values (and H) into the
     cache. With ``advance`` the cache's bookkeeping then counts the new tokens
     (their host timestamps: ``ts_host``, else copied from ``ts``)."""
-    import torch
     dev, d = x.device, x.shape[1]
     dt = _dtype_code(x)
     h = _Host(taus, d, rope_base, cu_new)
     arr = _enc_layers(layers)
     if h_out is None:
-        h_out = torch.empty_like(x)
+        h_out = _new(stream, x.shape, x.dtype, dev)
     if ws is None:
-        ws = _workspace(append_workspace_size(dt, taus, d, cu_new, layers, rope_base), dev)
+        ws = _workspace(append_workspace_size(dt, taus, d, cu_new, layers, rope_base), dev, stream)
     cst, keep = cache.struct()
     err = _err_word(dev, stream)
     _check(_lib.rest_encoder_append(dt, ctypes.byref(h.heads), ctypes.byref(h.batch), _ptr(x), _ptr(ts), arr,
@@ -488,13 +500,13 @@ def attn_forward(q, k, v, cu_seqlens, n_heads: int, o=None, o_lo=None, lse=None,
     dt = _dtype_code(q)
     h = _Host(np.zeros(n_heads, dtype=np.int64), d, 10000.0, cu_seqlens)
     if o is None:
-        o = torch.empty_like(q)
+        o = _new(stream, q.shape, q.dtype, dev)
     if o_lo is None and dt == REST_BF16:
-        o_lo = torch.empty_like(q)
+        o_lo = _new(stream, q.shape, q.dtype, dev)
     if lse is None:
-        lse = torch.empty((T, n_heads), dtype=torch.float32, device=dev)
+        lse = _new(stream, (T, n_heads), torch.float32, dev)
     if ws is None:
-        ws = _workspace(attn_workspace_size(dt, n_heads, d // n_heads, cu_seqlens), dev)
+        ws = _workspace(attn_workspace_size(dt, n_heads, d // n_heads, cu_seqlens), dev, stream)
     err = _err_word(dev, stream)
     _check(_lib.rest_attn_forward(dt, ctypes.byref(h.heads), ctypes.byref(h.batch), _ptr(q), _ptr(k), _ptr(v),
                                   _ptr(o), _ptr(o_lo), _ptr(lse), _ptr(ws), ws.numel(), _ptr(err),
@@ -511,11 +523,11 @@ def attn_backward(q, k, v, o, o_lo, lse, d_o, cu_seqlens, n_heads: int, dq=None,
     dev, (T, d) = q.device, q.shape
     dt = _dtype_code(q)
     h = _Host(np.zeros(n_heads, dtype=np.int64), d, 10000.0, cu_seqlens)
-    dq = torch.empty((T, d), dtype=torch.float32, device=dev) if dq is None else dq
-    dk = torch.empty((T, d), dtype=torch.float32, device=dev) if dk is None else dk
-    dv = torch.empty((T, d), dtype=torch.float32, device=dev) if dv is None else dv
+    dq = _new(stream, (T, d), torch.float32, dev) if dq is None else dq
+    dk = _new(stream, (T, d), torch.float32, dev) if dk is None else dk
+    dv = _new(stream, (T, d), torch.float32, dev) if dv is None else dv
     if ws is None:
-        ws = _workspace(attn_workspace_size(dt, n_heads, d // n_heads, cu_seqlens), dev)
+        ws = _workspace(attn_workspace_size(dt, n_heads, d // n_heads, cu_seqlens), dev, stream)
     err = _err_word(dev, stream)
     _check(_lib.rest_attn_backward(dt, ctypes.byref(h.heads), ctypes.byref(h.batch), _ptr(q), _ptr(k), _ptr(v),
                                    _ptr(o), _ptr(o_lo), _ptr(lse), _ptr(d_o), _ptr(dq), _ptr(dk), _ptr(dv),
@@ -534,10 +546,7 @@ def attn_backward(q, k, v, o, o_lo, lse, d_o, cu_seqlens, n_heads: int, dq=None,
 # synchronizes; with ``check=False`` nothing synchronizes, the call can be
 # captured into a CUDA graph, and ``err`` (an int32 tensor of one element)
 # receives the status if it is given. What a call allocates (outputs and
-# workspace that are not given) is ``stream``'s memory: the caching allocator
-# hands a freed block out again at once for the stream that it was allocated on,
-# whose earlier kernels ``stream`` does not wait for. Outputs are kept for the
-# current stream's use too.
+# workspace that are not given) is ``stream``'s memory.
 
 
 def _expect(name: str, t, dtype, shape, device) -> None:
@@ -557,23 +566,6 @@ def _expect_ws(ws, device) -> None:
         raise ValueError(f"ws is on {ws.device}, expected {device}")
     if not ws.is_contiguous():
         raise ValueError("ws must be contiguous")
-
-
-def _new(stream, shape, dtype, device, output: bool = True):
-    """An uninitialised tensor for a call on ``stream``."""
-    import torch
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=device)
-    if output:
-        t.record_stream(torch.cuda.current_stream(device))
-    return t
-
-
-def _new_ws(stream, nbytes: int, device):
-    import torch
-    return _new(stream, max(nbytes, 256), torch.uint8, device, output=False)
 
 
 def _run(fn, device, stream, check: bool, err, *args) -> None:
@@ -657,7 +649,7 @@ def embed_backward(d_out, ids, n_rows: int, scale: float = 1.0, d_table=None, ac
     else:
         _expect("d_table", d_table, torch.float32, (n_rows, d), dev)
     if ws is None:
-        ws = _new_ws(stream, embed_workspace_size(n_rows, d, T), dev)
+        ws = _workspace(embed_workspace_size(n_rows, d, T), dev, stream)
     else:
         _expect_ws(ws, dev)
     _run(_lib.rest_embed_backward, dev, stream, check, err, dt, n_rows, d, d_out.data_ptr(), T, ids.data_ptr(),
@@ -764,7 +756,6 @@ def decay_attn_forward(q, k, v, cu_seqlens, heads: DecayHeads, ts=None, state: O
     """Decay attention over packed histories: o [T, d] in q's dtype. With
     ``state`` user u continues the history of slot ``slots[u]`` (int32, on the
     device; default slot u), which then holds the new tokens too."""
-    import torch
     T = q.shape[0]
     dev, dt = _decay_inputs(T, heads, q, k, v, ts)
     cu, batch = _packed_batch(cu_seqlens, T)
@@ -774,7 +765,7 @@ def decay_attn_forward(q, k, v, cu_seqlens, heads: DecayHeads, ts=None, state: O
     else:
         _expect("o", o, q.dtype, q.shape, dev)
     if ws is None:
-        ws = _new_ws(stream, decay_attn_workspace_size(dt, heads, cu), dev)
+        ws = _workspace(decay_attn_workspace_size(dt, heads, cu), dev, stream)
     else:
         _expect_ws(ws, dev)
     _run(_lib.rest_decay_attn_forward, dev, stream, check, err, dt, heads.heads, heads.decay,
@@ -786,7 +777,6 @@ def decay_attn_forward(q, k, v, cu_seqlens, heads: DecayHeads, ts=None, state: O
 def decay_attn_backward(q, k, v, d_o, cu_seqlens, heads: DecayHeads, ts=None, dq=None, dk=None, dv=None, ws=None,
                         stream=None, check=True, err=None):
     """Gradients (dq, dk, dv), in q's dtype, of ``decay_attn_forward`` over histories that start empty."""
-    import torch
     T = q.shape[0]
     dev, dt = _decay_inputs(T, heads, q, k, v, ts)
     _expect("d_o", d_o, q.dtype, q.shape, dev)
@@ -799,7 +789,7 @@ def decay_attn_backward(q, k, v, d_o, cu_seqlens, heads: DecayHeads, ts=None, dq
             _expect(name, t, q.dtype, q.shape, dev)
         grads.append(t)
     if ws is None:
-        ws = _new_ws(stream, decay_attn_workspace_size(dt, heads, cu), dev)
+        ws = _workspace(decay_attn_workspace_size(dt, heads, cu), dev, stream)
     else:
         _expect_ws(ws, dev)
     _run(_lib.rest_decay_attn_backward, dev, stream, check, err, dt, heads.heads, heads.decay,
@@ -813,7 +803,6 @@ def decay_attn_step(q, k, v, state: DecayState, ts=None, slots=None, o=None, str
     """One new token for each of n histories: o [n, d]; row b continues slot
     ``slots[b]`` of ``state`` (int32, on the device; default slot b; -1 skips
     the row and leaves its o as it was), which then holds the token too."""
-    import torch
     n, heads = q.shape[0], state.heads
     dev, dt = _decay_inputs(n, heads, q, k, v, ts)
     st, sl = _decay_slots(n, state, slots, heads, dev)
@@ -869,11 +858,11 @@ def score_head(z, y, sp: dict, f_out=None, score_out=None, ws=None, stream=None,
     dt = _dtype_code(z)
     d_ff = int(sp["w_ffn2"].shape[1])
     if f_out is None:
-        f_out = torch.empty((N, K, d), dtype=torch.float32, device=dev)
+        f_out = _new(stream, (N, K, d), torch.float32, dev)
     if score_out is None:
-        score_out = torch.empty((N,), dtype=torch.float32, device=dev)
+        score_out = _new(stream, (N,), torch.float32, dev)
     if ws is None:
-        ws = _workspace(score_workspace_size(dt, d, K, N, d_ff), dev)
+        ws = _workspace(score_workspace_size(dt, d, K, N, d_ff), dev, stream)
     params = ScoreParams(_ptr(sp["w_ffn13"]), _ptr(sp["w_ffn2"]), _ptr(sp["ln_g"]), _ptr(sp["ln_b"]),
                          _ptr(sp["w_s"]), float(sp["b_s"]), d_ff)
     err = _err_word(dev, stream)
