@@ -268,12 +268,15 @@ def _err_word(device, stream=None):
     return w
 
 
-def check_device_error(err) -> None:
-    """Synchronize and raise if a kernel reported an error in the status word."""
-    code = int(err.item())
-    if code != 0:
-        err.zero_()  # the word is kept for later calls: leave it clear even for one that enqueues nothing
-        raise RestError(code, "device")
+def check_device_error(err, stream=None) -> None:
+    """Synchronize ``stream`` (default: the current one) and raise if a kernel on
+    it reported an error in the status word."""
+    import torch
+    with torch.cuda.stream(stream):
+        code = int(err.item())
+        if code != 0:
+            err.zero_()  # the word is kept for later calls: leave it clear even for one that enqueues nothing
+            raise RestError(code, "device")
 
 
 def rotation_table(ts, cu_seqlens, taus, head_dim: int, rope_base: float = 10000.0, stream=None, check=True):
@@ -290,7 +293,7 @@ def rotation_table(ts, cu_seqlens, taus, head_dim: int, rope_base: float = 10000
     _check(_lib.rest_rotation_table(ctypes.byref(h.heads), ctypes.byref(h.batch), _ptr(ts), _ptr(idx), _ptr(cos),
                                     _ptr(sin), _ptr(ws), ws.numel(), _ptr(err), _stream(stream)), "rest_rotation_table")
     if check:
-        check_device_error(err)
+        check_device_error(err, stream)
     return idx, cos, sin
 
 
@@ -310,7 +313,7 @@ def encoder_attn(x, ts, cu_seqlens, taus, layers: Sequence[dict], l_switch: int,
                                   len(layers), l_switch, _ptr(h_out), _ptr(ws), ws.numel(), _ptr(err),
                                   _stream(stream)), "rest_encoder_attn")
     if check:
-        check_device_error(err)
+        check_device_error(err, stream)
     return h_out
 
 
@@ -338,7 +341,7 @@ def cross_decode(hmem, cu_seqlens, taus, reqs, z, dec: dict, rope_base: float = 
                                   _ptr(z), ctypes.byref(dp), _ptr(y_out), _ptr(ws), ws.numel(), _ptr(err),
                                   _stream(stream)), "rest_cross_decode")
     if check:
-        check_device_error(err)
+        check_device_error(err, stream)
     return y_out
 
 
@@ -367,7 +370,7 @@ def cross_decode_static_ws(hmem, cu_seqlens, taus, reqs, z, dec: dict, rope_base
                                             ctypes.byref(h.reqs), _ptr(z), ctypes.byref(dp), _ptr(y_out), _ptr(err),
                                             _stream(stream)), "rest_cross_decode_static_ws")
     if check:
-        check_device_error(err)
+        check_device_error(err, stream)
     return y_out
 
 
@@ -391,7 +394,7 @@ def rank_request(x, ts, cu_seqlens, taus, layers: Sequence[dict], l_switch: int,
                                   len(layers), l_switch, ctypes.byref(h.reqs), _ptr(z), ctypes.byref(dp), _ptr(h_out),
                                   _ptr(y_out), _ptr(ws), ws.numel(), _ptr(err), _stream(stream)), "rest_rank_request")
     if check:
-        check_device_error(err)
+        check_device_error(err, stream)
     return h_out, y_out
 
 
@@ -476,7 +479,7 @@ def encoder_append(x, ts, cu_new, taus, layers: Sequence[dict], l_switch: int, c
                                     _ptr(err), _stream(stream)), "rest_encoder_append")
     del keep
     if check:
-        check_device_error(err)
+        check_device_error(err, stream)
     if advance:
         cache.advance(cu_new, ts.cpu().numpy() if ts_host is None else ts_host)
     return h_out
@@ -512,7 +515,7 @@ def attn_forward(q, k, v, cu_seqlens, n_heads: int, o=None, o_lo=None, lse=None,
                                   _ptr(o), _ptr(o_lo), _ptr(lse), _ptr(ws), ws.numel(), _ptr(err),
                                   _stream(stream)), "rest_attn_forward")
     if check:
-        check_device_error(err)
+        check_device_error(err, stream)
     return o, o_lo, lse
 
 
@@ -533,7 +536,7 @@ def attn_backward(q, k, v, o, o_lo, lse, d_o, cu_seqlens, n_heads: int, dq=None,
                                    _ptr(o), _ptr(o_lo), _ptr(lse), _ptr(d_o), _ptr(dq), _ptr(dk), _ptr(dv),
                                    _ptr(ws), ws.numel(), _ptr(err), _stream(stream)), "rest_attn_backward")
     if check:
-        check_device_error(err)
+        check_device_error(err, stream)
     return dq, dk, dv
 
 
@@ -595,11 +598,7 @@ def _run(fn, device, stream, check: bool, err, *args) -> None:
     else:
         _expect("err", err, torch.int32, (1,), device)
     _check(fn(*args, err.data_ptr(), handle), fn.__name__)
-    if stream is None:
-        check_device_error(err)
-    else:
-        with torch.cuda.stream(stream):
-            check_device_error(err)
+    check_device_error(err, stream)
 
 
 def _cuda_device(t):
@@ -869,7 +868,7 @@ def score_head(z, y, sp: dict, f_out=None, score_out=None, ws=None, stream=None,
     _check(_lib.rest_score_head(dt, d, K, N, _ptr(z), _ptr(y), ctypes.byref(params), _ptr(f_out), _ptr(score_out),
                                 _ptr(ws), ws.numel(), _ptr(err), _stream(stream)), "rest_score_head")
     if check:
-        check_device_error(err)
+        check_device_error(err, stream)
     return f_out, score_out
 
 

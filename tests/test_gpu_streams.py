@@ -1,4 +1,6 @@
-"""Calls on a stream of their own: what they allocate is that stream's memory."""
+"""Calls on a stream of their own: what they allocate is that stream's memory,
+and with ``check`` they wait for that stream before they read its status."""
+
 import pytest
 import torch
 
@@ -7,6 +9,19 @@ import workloads as W
 
 pytestmark = pytest.mark.gpu
 
+def test_the_status_is_read_on_the_calls_stream(cuda):
+    other = torch.cuda.Stream()
+    ts = torch.tensor([5, 9, 3], device=cuda)
+    big = torch.randn(8192, 8192, device=cuda)
+    R.rotation_table(ts.sort()[0], [0, 3], (0, 1), 16, stream=other)
+    with torch.cuda.stream(other):
+        out = big @ big
+        torch.cuda.synchronize()
+        for _ in range(8):
+            torch.mm(big, big, out=out)        # the call's kernels wait behind these
+    with pytest.raises(R.RestError) as e:
+        R.rotation_table(ts, [0, 3], (0, 1), 16, stream=other)
+    assert e.value.status == 2
 
 def _calls(cuda):
     w = W.small_workload("bf16", lengths=(200, 37), d=128, n_heads=4, n_layers=1, l_switch=0,
@@ -29,7 +44,6 @@ def _calls(cuda):
                                                             t["z"], t["dec"], **base, **kw)),
             "attn_forward": (0, lambda **kw: R.attn_forward(*q[:3], cu, 4, **kw)),
             "attn_backward": (0, lambda **kw: R.attn_backward(*q[:3], *attn, q[3], cu, 4, **kw))}
-
 
 @pytest.mark.parametrize("name", ["rotation_table", "encoder_attn", "encoder_append", "cross_decode", "rank_request",
                                   "attn_forward", "attn_backward"])
