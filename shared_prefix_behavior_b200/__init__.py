@@ -658,43 +658,65 @@ def embed_backward(d_out, ids, n_rows: int, scale: float = 1.0, d_table=None, ac
 
 class DecayHeads:
     """The heads of decay attention: granularity (0: a position head, else the
-    bucket in seconds) and log decay (<= 0, per token or per bucket) of each."""
+    bucket in seconds) and log decay (<= 0, per token or per bucket) of each.
+    The calls read both arrays where they are, so they are not replaced."""
 
     def __init__(self, taus, log_decay, head_dim: int):
-        self.taus = np.array(taus, dtype=np.int64).reshape(-1)
-        self.log_decay = np.array(log_decay, dtype=np.float64).reshape(-1)
+        self._taus = np.array(taus, dtype=np.int64).reshape(-1)
+        self._log_decay = np.array(log_decay, dtype=np.float64).reshape(-1)
         if len(self.taus) != len(self.log_decay) or len(self.taus) == 0:
             raise ValueError("taus and log_decay need one entry for each head")
         self.n_heads, self.head_dim = len(self.taus), int(head_dim)
         self.d = self.n_heads * self.head_dim
-        self.timed = bool((self.taus > 0).any())
         self._heads = Heads(self.d, self.n_heads, self.head_dim, self.taus.ctypes.data_as(POINTER(c_int64)), 10000.0)
         self.heads = ctypes.addressof(self._heads)
         self.decay = self.log_decay.ctypes.data
 
+    @property
+    def taus(self) -> np.ndarray:
+        return self._taus
+
+    @property
+    def log_decay(self) -> np.ndarray:
+        return self._log_decay
+
+    @property
+    def timed(self) -> bool:
+        return bool((self._taus > 0).any())
+
 
 class DecayState:
     """Cached states of ``n_slots`` histories: ``s`` fp32 [n_slots, n_heads,
-    head_dim, head_dim], and the tokens absorbed and the first and last
-    timestamp of each (int64 [n_slots]), all on the device."""
+    head_dim, head_dim], and ``len``, ``t_first`` and ``t_last`` int64 [n_slots],
+    the tokens absorbed and the first and last timestamp of each, all on the
+    device. Tensors of the same kind may be assigned in their place."""
 
     def __init__(self, heads: DecayHeads, n_slots: int, device=None, tensors=None):
         import torch
         self.heads, self.n_slots = heads, int(n_slots)
-        shape = (self.n_slots, heads.n_heads, heads.head_dim, heads.head_dim)
+        self._shape = (self.n_slots, heads.n_heads, heads.head_dim, heads.head_dim)
         if tensors is None:
-            self.s = torch.zeros(shape, dtype=torch.float32, device=device)
-            self.len, self.t_first, self.t_last = (torch.zeros(self.n_slots, dtype=torch.int64, device=device)
-                                                   for _ in range(3))
-        else:
-            self.s, self.len, self.t_first, self.t_last = tensors
-        _cuda_device(self.s)
-        _expect("s", self.s, torch.float32, shape, self.s.device)
-        for name in ("len", "t_first", "t_last"):
-            _expect(name, getattr(self, name), torch.int64, (self.n_slots,), self.s.device)
-        self._struct = DecayStateStruct(self.s.data_ptr(), self.len.data_ptr(), self.t_first.data_ptr(),
-                                        self.t_last.data_ptr(), self.n_slots)
+            s = torch.zeros(self._shape, dtype=torch.float32, device=device)
+            tensors = (s, *(torch.zeros(self.n_slots, dtype=torch.int64, device=device) for _ in range(3)))
+        self._device = _cuda_device(tensors[0])
+        self._struct = DecayStateStruct(None, None, None, None, self.n_slots)
         self.struct = ctypes.addressof(self._struct)
+        self.s, self.len, self.t_first, self.t_last = tensors
+
+    def _put(self, name: str, t) -> None:
+        """Takes ``t`` as the array ``name``, for the calls too, which read its address."""
+        import torch
+        if name == "s":
+            _expect(name, t, torch.float32, self._shape, self._device)
+        else:
+            _expect(name, t, torch.int64, (self.n_slots,), self._device)
+        setattr(self, "_" + name, t)
+        setattr(self._struct, name, t.data_ptr())
+
+    s = property(lambda self: self._s, lambda self, t: self._put("s", t))
+    len = property(lambda self: self._len, lambda self, t: self._put("len", t))
+    t_first = property(lambda self: self._t_first, lambda self, t: self._put("t_first", t))
+    t_last = property(lambda self: self._t_last, lambda self, t: self._put("t_last", t))
 
     def reset(self) -> None:
         """Every slot holds an empty history from here on (on the current stream)."""

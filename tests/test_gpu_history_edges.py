@@ -269,3 +269,32 @@ def test_outputs_on_another_stream_outlive_their_use_on_the_current_one(cuda):
     assert again.data_ptr() != where
     torch.cuda.synchronize()
     assert torch.equal(kept, want) and torch.equal(again, want)
+
+
+# ---------------------------------------------------------------- states
+
+
+def test_decay_state_takes_assigned_tensors(cuda):
+    """A restored checkpoint, assigned as it is: the calls use it, and what it replaces stays as it was."""
+    torch.manual_seed(2)
+    heads = R.DecayHeads((0, 1), (-0.1, -0.2), 16)
+    x, ts = torch.randn(2, 3, 32, device=cuda), [torch.tensor(t, device=cuda) for t in ([10, 20, 30], [15, 21, 40])]
+    state = R.DecayState(heads, 3, device=cuda)
+    R.decay_attn_step(x[0], x[0], x[0], state, ts=ts[0])
+    saved = [t.clone() for t in (state.s, state.len, state.t_first, state.t_last)]
+    want = R.decay_attn_step(x[1], x[1], x[1], state, ts=ts[1])
+    old = [state.s, state.len, state.t_first, state.t_last]
+    ended = [t.clone() for t in old]
+    state.s, state.len, state.t_first, state.t_last = [t.clone() for t in saved]
+    assert torch.equal(R.decay_attn_step(x[1], x[1], x[1], state, ts=ts[1]), want)
+    assert all(torch.equal(a, b) for a, b in zip((state.s, state.len, state.t_first, state.t_last), ended))
+    assert all(torch.equal(a, b) for a, b in zip(old, ended))
+    state.s, state.len, state.t_first, state.t_last = [t.clone() for t in saved]
+    o = R.decay_attn_forward(x[1], x[1], x[1], [0, 1, 2, 3], heads, ts=ts[1], state=state)
+    # a one-row pass and the step: 12 u32 for each of the pass's products on the tensor pipe, and its weights'
+    assert torch.all((o - want).abs() <= 200 * U32 * want.abs().max())
+    assert all(torch.equal(a, b) for a, b in zip(old, ended))
+    for name, bad in (("s", saved[0][:2]), ("s", saved[0].double()), ("len", saved[1].int()), ("t_last", saved[3].cpu())):
+        with pytest.raises((TypeError, ValueError)):
+            setattr(state, name, bad)
+    assert state.s.shape == (3, 2, 16, 16)

@@ -9,6 +9,7 @@ import workloads as W
 
 pytestmark = pytest.mark.gpu
 
+
 def test_the_status_is_read_on_the_calls_stream(cuda):
     other = torch.cuda.Stream()
     ts = torch.tensor([5, 9, 3], device=cuda)
