@@ -357,7 +357,8 @@ rest_status rest_score_head(rest_dtype dt, int d, int K, long long n_cands, cons
 
 /* ------------------------------------------------------------------ item ids
  * A history token names an item: its feature vector s_i, a row of the
- * encoder's input x, is the item's row of an embedding table. */
+ * encoder's input x, is the item's row of an embedding table. These calls and
+ * those of decay attention clear *dev_err also when they have nothing to do. */
 
 /* Embedding lookup: out[t] = scale * table[ids[t]], the product taken in fp32
  * and rounded once to the call's dtype. An id of -1 is padding: its row of out

@@ -1403,6 +1403,14 @@ rest_status rest_score_head(rest_dtype dt, int d, int K, long long n_cands, cons
 
 // ---------------------------------------------------------------- item ids
 
+// A call with nothing to do still leaves its own status in the caller's word
+static rest_status empty_call(int32_t* dev_err, void* stream) {
+  if (!dev_err) return REST_OK;
+  rest_status st = check_device();
+  if (st != REST_OK) return st;
+  return cudaMemsetAsync(dev_err, 0, sizeof(int32_t), (cudaStream_t)stream) == cudaSuccess ? REST_OK : REST_ERR_CUDA;
+}
+
 static rest_status check_embed(long long n_rows, int d, long long n_tokens) {
   if (n_rows < 1 || n_tokens < 0 || d < 8 || d % 8 != 0) return REST_ERR_INVALID_ARG;
   if (n_rows >= (1LL << 31) - 1 || n_tokens >= (1LL << 30) || d > 8192 || n_tokens * d >= (1LL << 40) ||
@@ -1421,7 +1429,7 @@ rest_status rest_embed_forward(rest_dtype dt, long long n_rows, int d, const voi
     if (n_tokens > 0)
       for (const void* p : {table, (const void*)ids, (const void*)out})
         if (!p || !aligned16(p)) return REST_ERR_INVALID_ARG;
-    if (n_tokens == 0) return REST_OK;
+    if (n_tokens == 0) return empty_call(dev_err, stream);
     if ((st = check_device()) != REST_OK) return st;
     cudaStream_t s = (cudaStream_t)stream;
     if (dev_err && cudaMemsetAsync(dev_err, 0, sizeof(int32_t), s) != cudaSuccess) return REST_ERR_CUDA;
@@ -1454,7 +1462,7 @@ rest_status rest_embed_backward(rest_dtype dt, long long n_rows, int d, const vo
     if (n_tokens > 0 && (!d_out || !ids || !aligned16(d_out) || !aligned16(ids))) return REST_ERR_INVALID_ARG;
     if (n_tokens > 0 && (!ws || !aligned16(ws) || ws_bytes < embed_backward_ws_bytes(n_rows, d, n_tokens)))
       return REST_ERR_WORKSPACE;
-    if (n_tokens == 0 && accumulate) return REST_OK;
+    if (n_tokens == 0 && accumulate) return empty_call(dev_err, stream);
     if ((st = check_device()) != REST_OK) return st;
     cudaStream_t s = (cudaStream_t)stream;
     if (dev_err && cudaMemsetAsync(dev_err, 0, sizeof(int32_t), s) != cudaSuccess) return REST_ERR_CUDA;
@@ -1699,7 +1707,7 @@ rest_status rest_decay_attn_forward(rest_dtype dt, const rest_heads* heads, cons
       for (const void* ptr : {q, k, v, (const void*)o})
         if (!ptr || !aligned16(ptr)) return REST_ERR_INVALID_ARG;
     if (!ws || ws_bytes < p.total || !aligned16(ws)) return REST_ERR_WORKSPACE;
-    if (p.T == 0) return REST_OK;
+    if (p.T == 0) return empty_call(dev_err, stream);
     if ((st = check_device()) != REST_OK) return st;
     cudaStream_t s = (cudaStream_t)stream;
     if ((st = decay_begin(p, heads, batch, ts, cached, ws, dev_err, &a, s)) != REST_OK) return st;
@@ -1734,7 +1742,7 @@ rest_status rest_decay_attn_backward(rest_dtype dt, const rest_heads* heads, con
       for (const void* ptr : {q, k, v, d_o, (const void*)dq, (const void*)dk, (const void*)dv})
         if (!ptr || !aligned16(ptr)) return REST_ERR_INVALID_ARG;
     if (!ws || ws_bytes < p.total || !aligned16(ws)) return REST_ERR_WORKSPACE;
-    if (p.T == 0) return REST_OK;
+    if (p.T == 0) return empty_call(dev_err, stream);
     if ((st = check_device()) != REST_OK) return st;
     cudaStream_t s = (cudaStream_t)stream;
     DecayState none;
@@ -1775,7 +1783,7 @@ rest_status rest_decay_attn_step(rest_dtype dt, const rest_heads* heads, const d
     if (n > 0)
       for (const void* ptr : {q, k, v, (const void*)o})
         if (!ptr || !aligned16(ptr)) return REST_ERR_INVALID_ARG;
-    if (n == 0) return REST_OK;
+    if (n == 0) return empty_call(dev_err, stream);
     if ((st = check_device()) != REST_OK) return st;
     cudaStream_t s = (cudaStream_t)stream;
     if (dev_err && cudaMemsetAsync(dev_err, 0, sizeof(int32_t), s) != cudaSuccess) return REST_ERR_CUDA;

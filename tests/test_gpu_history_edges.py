@@ -298,3 +298,21 @@ def test_decay_state_takes_assigned_tensors(cuda):
         with pytest.raises((TypeError, ValueError)):
             setattr(state, name, bad)
     assert state.s.shape == (3, 2, 16, 16)
+
+
+def test_a_call_with_nothing_to_do_clears_the_status(cuda):
+    """The word of an earlier call, whose error was not read, is not the empty call's."""
+    heads = R.DecayHeads((0, 8), (-0.1, -0.1), 16)
+    state = R.DecayState(heads, 2, device=cuda)
+    x, i = torch.empty(0, 32, device=cuda), torch.empty(0, dtype=torch.int64, device=cuda)
+    g = torch.zeros(4, 32, device=cuda)
+    for call in (lambda **kw: R.embed_forward(g, i, **kw), lambda **kw: R.embed_backward(x, i, 4, **kw),
+                 lambda **kw: R.embed_backward(x, i, 4, d_table=g, accumulate=True, **kw),
+                 lambda **kw: R.decay_attn_forward(x, x, x, [0, 0], heads, ts=i, **kw),
+                 lambda **kw: R.decay_attn_backward(x, x, x, x, [0, 0], heads, ts=i, **kw),
+                 lambda **kw: R.decay_attn_step(x, x, x, state, ts=i, **kw)):
+        err = torch.full((1,), 2, dtype=torch.int32, device=cuda)
+        call(err=err, check=False)
+        assert int(err) == 0
+        err.fill_(2)
+        call(err=err)
