@@ -431,7 +431,12 @@ typedef struct {
   int n_slots;
 } rest_decay_state;
 
-/* Workspace bytes rest_decay_attn_forward and rest_decay_attn_backward need. */
+/* Workspace bytes with which rest_decay_attn_forward and rest_decay_attn_backward
+ * are fastest for this batch. It is not the larger for a larger batch: few
+ * histories are cut into segments with states between them. A smaller workspace
+ * leaves histories in fewer segments, which takes longer; REST_ERR_WORKSPACE
+ * only below what every batch of as many users needs. So the size for one batch
+ * is enough for every batch of no more users. */
 rest_status rest_decay_attn_workspace_size(rest_dtype dt, const rest_heads* heads, const rest_batch* batch,
                                            size_t* bytes);
 

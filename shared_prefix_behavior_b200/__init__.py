@@ -765,6 +765,8 @@ def _packed_batch(cu_seqlens, T):
 
 
 def decay_attn_workspace_size(dtype: int, heads: DecayHeads, cu_seqlens) -> int:
+    """Workspace bytes with which a pass over this batch is fastest. A pass takes
+    any workspace that is the size for some batch of at least as many users."""
     cu, batch = _packed_batch(cu_seqlens, None)
     out = c_size_t(0)
     _check(_lib.rest_decay_attn_workspace_size(dtype, heads.heads, ctypes.addressof(batch), ctypes.byref(out)),

@@ -1526,6 +1526,21 @@ struct DecayPlan {
 
 constexpr int DECAY_BLOCK = 64;
 
+// Where a plan's arrays lie in the workspace, and its bytes. The part that does
+// not depend on the cut grows with the number of users alone.
+static size_t decay_layout(const rest_heads* hs, int n_users, bool back, long long n_items, long long n_parts,
+                           DecayPlan* p) {
+  const size_t per = (size_t)(back ? 2 : 1) * n_parts * hs->n_heads;  // backward: both directions
+  size_t off = 0;
+  auto take = [&](size_t bytes) { size_t o = off; off = align_up(off + bytes, 256); return o; };
+  p->items = take(sizeof(DecayItem) * (size_t)std::max<long long>(n_items, n_users));
+  p->parts = take(sizeof(DecayPart) * (size_t)n_parts);
+  p->users = take(sizeof(DecayUser) * (size_t)n_users);
+  p->state = take(4 * per * hs->head_dim * hs->head_dim);
+  p->decay = take(4 * per);
+  return p->total = off;
+}
+
 // A kernel's time in us: a 64-row block takes one resident CTA `alone` and each of
 // `per_sm` together `full`, and a CTA `fixed` besides (its first loads, the state
 // in and out). The numbers are fitted to 2,185 calls of given segments (117
@@ -1553,7 +1568,8 @@ static double decay_time(const DecayCost& c, const DecayLoad& l) {
 // Rows of a segment and its parts. More segments fill the GPU and shorten the
 // longest one, but the states between them are computed in a launch of its
 // own, joined, and read back; that launch has work for more CTAs of fewer rows.
-static DecayCut decay_cut(rest_dtype dt, const rest_heads* hs, const rest_batch* b, bool back) {
+// The states have to fit into ws_bytes; uncut histories need none.
+static DecayCut decay_cut(rest_dtype dt, const rest_heads* hs, const rest_batch* b, bool back, size_t ws_bytes) {
   const bool wide = hs->head_dim == 64;
   static const struct { DecayCost own, pass, dkdv; } costs[2][2] = {
       {{{7, 2.2, 2.2, 0.9}, {3, 4.0, 8.5, 0.3}, {2, 6.7, 10.0, 1.3}},     // fp32, head_dim 16 and 32
@@ -1583,17 +1599,22 @@ static DecayCut decay_cut(rest_dtype dt, const rest_heads* hs, const rest_batch*
       const int part = ((whole + cuts - 1) / cuts + m - 1) / m, rows = part * m;  // in blocks
       DecayLoad load{0, 0, (double)rows, 0, 0};
       double parts = 0, joined = 0;  // parts: whose own states are wanted
+      long long n_items = 0, n_parts = 0;
       for (const auto& l : lengths) {
         const int k = (l.first + rows - 1) / rows, rest = l.first % rows;
         load.full += l.first / rows * H * l.second;
         load.shorts += (rest > 0 ? 1 : 0) * H * l.second;
         load.short_blocks += rest * H * l.second;
         load.longest_short = std::max(load.longest_short, (double)rest);
+        n_items += (long long)k * l.second;
         if (k > 1) {
+          n_parts += (long long)((l.first + part - 1) / part) * l.second;
           parts += (double)(k - 1) * m * l.second;
           joined = (double)k * m;
         }
       }
+      DecayPlan layout;
+      if (cuts > 1 && decay_layout(hs, b->n_users, back, n_items, n_parts, &layout) > ws_bytes) continue;
       double t = decay_time(cost.pass, load);
       if (back) t += decay_time(cost.dkdv, load);
       if (parts > 0) {
@@ -1610,12 +1631,13 @@ static DecayCut decay_cut(rest_dtype dt, const rest_heads* hs, const rest_batch*
   return best;
 }
 
-static rest_status decay_plan(rest_dtype dt, const rest_heads* hs, const rest_batch* b, bool back, DecayPlan* p) {
+static rest_status decay_plan(rest_dtype dt, const rest_heads* hs, const rest_batch* b, bool back, size_t ws_bytes,
+                              DecayPlan* p) {
   rest_status st = check_heads(dt, hs);
   if (st != REST_OK) return st;
   if ((st = check_batch(b, &p->T)) != REST_OK) return st;
   if (p->T >= (1LL << 30)) return REST_ERR_UNSUPPORTED;
-  p->cut = decay_cut(dt, hs, b, back);
+  p->cut = decay_cut(dt, hs, b, back, ws_bytes);
   p->n_items = p->n_parts = 0;
   const int of_part = p->cut.rows / p->cut.m;
   for (int u = 0; u < b->n_users; ++u) {
@@ -1625,15 +1647,7 @@ static rest_status decay_plan(rest_dtype dt, const rest_heads* hs, const rest_ba
     p->n_items += n;
     p->n_parts += n > 1 ? (rows + of_part - 1) / of_part : 0;
   }
-  const size_t per = (size_t)(back ? 2 : 1) * p->n_parts * hs->n_heads;  // backward: both directions
-  size_t off = 0;
-  auto take = [&](size_t bytes) { size_t o = off; off = align_up(off + bytes, 256); return o; };
-  p->items = take(sizeof(DecayItem) * (size_t)p->n_items);
-  p->parts = take(sizeof(DecayPart) * (size_t)p->n_parts);
-  p->users = take(sizeof(DecayUser) * (size_t)b->n_users);
-  p->state = take(4 * per * hs->head_dim * hs->head_dim);
-  p->decay = take(4 * per);
-  p->total = off;
+  decay_layout(hs, b->n_users, back, p->n_items, p->n_parts, p);
   return REST_OK;
 }
 
@@ -1681,9 +1695,9 @@ rest_status rest_decay_attn_workspace_size(rest_dtype dt, const rest_heads* head
   if (!bytes) return REST_ERR_INVALID_ARG;
   try {
     DecayPlan fwd, back;
-    rest_status st = decay_plan(dt, heads, batch, false, &fwd);
+    rest_status st = decay_plan(dt, heads, batch, false, SIZE_MAX, &fwd);
     if (st != REST_OK) return st;
-    if ((st = decay_plan(dt, heads, batch, true, &back)) != REST_OK) return st;
+    if ((st = decay_plan(dt, heads, batch, true, SIZE_MAX, &back)) != REST_OK) return st;
     *bytes = std::max(fwd.total, back.total);
     return REST_OK;
   } catch (...) {
@@ -1697,7 +1711,7 @@ rest_status rest_decay_attn_forward(rest_dtype dt, const rest_heads* heads, cons
                                     void* ws, size_t ws_bytes, int32_t* dev_err, void* stream) {
   try {
     DecayPlan p;
-    rest_status st = decay_plan(dt, heads, batch, false, &p);
+    rest_status st = decay_plan(dt, heads, batch, false, ws ? ws_bytes : 0, &p);
     if (st != REST_OK) return st;
     DecayArgs a;
     DecayState cached;
@@ -1734,7 +1748,7 @@ rest_status rest_decay_attn_backward(rest_dtype dt, const rest_heads* heads, con
                                      size_t ws_bytes, int32_t* dev_err, void* stream) {
   try {
     DecayPlan p;
-    rest_status st = decay_plan(dt, heads, batch, true, &p);
+    rest_status st = decay_plan(dt, heads, batch, true, ws ? ws_bytes : 0, &p);
     if (st != REST_OK) return st;
     DecayArgs a;
     if ((st = check_decay(dt, heads, log_decay, ts, p.T > 0, &a.h)) != REST_OK) return st;

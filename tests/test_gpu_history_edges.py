@@ -316,3 +316,62 @@ def test_a_call_with_nothing_to_do_clears_the_status(cuda):
         assert int(err) == 0
         err.fill_(2)
         call(err=err)
+
+
+# ---------------------------------------------------------------- workspaces
+
+
+def _launched(call):
+    R.profile_begin()
+    out = call()
+    return out, {x["name"]: x["launches"] for x in R.profile_end()}
+
+
+@pytest.mark.parametrize("dtype,hd,lengths", [("f32", 64, (1500,)), ("bf16", 32, (1500, 0, 700, 3)), ("f32", 16, (2000, 1000))])
+def test_decay_in_a_smaller_workspace(cuda, dtype, hd, lengths):
+    """The fastest cut's workspace, part of it, and the least: fewer segments, the
+    same results within their bounds, nothing written behind the workspace."""
+    (q, k, v, d_o), ts, cu, taus, decay = _case(dtype, hd, lengths, 3)
+    heads = R.DecayHeads(taus, decay, hd)
+    t, tts, L = [_dev(x, dtype) for x in (q, k, v, d_o)], torch.from_numpy(ts).to(cuda), max(lengths)
+    want, S = O.decay_attention(q, k, v, ts, cu, taus, decay)
+    mag, Smag = O.decay_attention(q, k, v, ts, cu, taus, decay, magnitude=True)
+    ref = O.decay_attention_backward(q, k, v, ts, cu, taus, decay, d_o)
+    big = O.decay_attention_backward(q, k, v, ts, cu, taus, decay, d_o, magnitude=True)
+    full = R.decay_attn_workspace_size(R.REST_BF16 if dtype == "bf16" else R.REST_F32, heads, cu)
+    least = R.decay_attn_workspace_size(R.REST_F32, heads, np.zeros(len(cu), dtype=np.int32))
+    assert least < full
+    seen = []
+    for size in (full, full // 2 // 16 * 16, least):
+        buf = torch.full((size + 4096,), 0xab, dtype=torch.uint8, device=cuda)
+        ws = buf[:size]
+        o, names = _launched(lambda: R.decay_attn_forward(*t[:3], cu, heads, ts=tts, ws=ws))
+        state = R.DecayState(heads, len(lengths), device=cuda)
+        o2 = R.decay_attn_forward(*t[:3], cu, heads, ts=tts, ws=ws, state=state)
+        g, back = _launched(lambda: R.decay_attn_backward(*t, cu, heads, ts=tts, ws=ws))
+        assert bool((buf[size:] == 0xab).all())
+        for a, b, m, what in ((o, want, mag, "o"), (o2, want, mag, "o with a state"), *zip(g, ref, big, ("dq", "dk", "dv"))):
+            if dtype == "bf16":
+                _rounded_once(a, b, m, L, hd, what)
+            else:
+                err = np.abs(a.cpu().numpy().astype(np.float64) - b)
+                assert np.all(err <= (L + 2 * hd + 64) * U32 * m), what
+        assert np.all(np.abs(state.s.cpu().numpy() - S) <= (L + 64) * U32 * Smag)
+        seen.append(("decay_parts" in names, "decay_parts" in back))
+    assert seen[0] == (True, True) and seen[-1] == (False, False)
+    with pytest.raises(R.RestError) as e:
+        R.decay_attn_forward(*t[:3], cu, heads, ts=tts, ws=torch.empty(least - 256, dtype=torch.uint8, device=cuda))
+    assert e.value.status == 6
+
+
+@pytest.mark.parametrize("dtype,hd,lengths", [("bf16", 32, (300,) * 90), ("f32", 32, (300,) * 90), ("bf16", 64, (200, 330) * 20)])
+def test_decay_histories_that_are_not_cut(cuda, dtype, hd, lengths):
+    """The histories that other tests take for uncut ones: the pass alone is launched."""
+    taus, decay = (0, 0, 0, 0, 1, 64, 4096, 65536), (-0.1, -0.01, -0.5, 0.0, -1e-5, -1e-3, -0.02, -0.3)
+    (q, k, v, d_o), ts, cu, taus, decay = _case(dtype, hd, lengths, 31, taus=taus, decay=decay)
+    heads = R.DecayHeads(taus, decay, hd)
+    t, tts = [_dev(x, dtype) for x in (q, k, v, d_o)], torch.from_numpy(ts).to(cuda)
+    _, names = _launched(lambda: R.decay_attn_forward(*t[:3], cu, heads, ts=tts))
+    assert set(names) - {"decay_prep"} == {"decay_pass"}
+    _, names = _launched(lambda: R.decay_attn_backward(*t, cu, heads, ts=tts))
+    assert set(names) - {"decay_prep"} == {"decay_pass", "decay_dkdv"}
