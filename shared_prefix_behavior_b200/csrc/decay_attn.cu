@@ -1,6 +1,5 @@
 // Decay attention: linear attention with a decay for each head.
 #include <algorithm>
-#include <atomic>
 
 #include "common.cuh"
 #include "history.h"
@@ -1353,19 +1352,12 @@ __global__ void __launch_bounds__(STEP_THREADS, 4) decay_step_kernel(DecayHeadsA
   }
 }
 
-// More than 48 KB a block, the kernel's static arrays included, need the
-// attribute: set once a device and kernel, to the most that was asked for.
-template <auto KERNEL>
-cudaError_t allow_smem(int bytes) {
-  static std::atomic<int> most[64];
-  int dev = 0;
-  if (bytes <= 40 * 1024) return cudaSuccess;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess || dev < 0 || dev >= 64) return e != cudaSuccess ? e : cudaErrorInvalidDevice;
-  if (most[dev].load(std::memory_order_relaxed) >= bytes) return cudaSuccess;
-  e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess) most[dev].store(bytes, std::memory_order_relaxed);
-  return e;
+// More than 48 KB a block need the kernel's attribute. Every launch sets it, to
+// one number a kernel, whatever the launch takes: calls from several threads
+// cannot lower one another's, and a new context of the device has it too.
+template <auto KERNEL, int BYTES>
+cudaError_t allow_smem() {
+  return cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES);
 }
 
 template <typename T, int HD>
@@ -1377,7 +1369,7 @@ cudaError_t step_hd(const DecayHeadsArg& hs, int n, const void* q, const void* k
   const int chunks = (hs.n_heads + G - 1) / G;
   int size = 1;
   while (size < 8 && size < chunks && (long long)n * size < 148 * 4) size *= 2;
-  cudaError_t e = allow_smem<decay_step_kernel<T, HD>>(bytes);
+  cudaError_t e = allow_smem<decay_step_kernel<T, HD>, bytes>();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
@@ -1413,11 +1405,15 @@ bool tile_maps(TileMaps* maps, const DecayArgs& a, const void* p0, const void* p
 // Fewer blocks than the SMs hold are spread evenly: the hardware puts a second
 // and third on some SMs and leaves others empty (256 blocks of 32 x 1024 rows: 24
 // SMs had three and 32 none). Shared memory that nothing uses keeps an SM to its share.
+constexpr int SPREAD_MOST = 227 * 1024, SPREAD_KERNEL = 5 * 1024;  // static arrays and the system's 1 KB
+constexpr int spread_even(int share) {  // share + 1 of these do not fit
+  return SPREAD_MOST / (share + 1) + 1 - SPREAD_KERNEL + 4 * 1024;
+}
 int spread_smem(int bytes, long long blocks) {
-  constexpr int SMS = 148, MOST = 227 * 1024, KERNEL = 5 * 1024;  // static arrays and the system's 1 KB
-  const int share = (int)std::min<long long>(32, (blocks + SMS - 1) / SMS);
-  const int even = MOST / (share + 1) + 1 - KERNEL + 4 * 1024;  // share + 1 of these do not fit
-  return (blocks + SMS - 1) / SMS > 4 || (long long)(even + KERNEL) * share > MOST ? bytes : std::max(bytes, even);
+  constexpr int SMS = 148;
+  const int share = (int)std::min<long long>(32, (blocks + SMS - 1) / SMS), even = spread_even(share);
+  return (blocks + SMS - 1) / SMS > 4 || (long long)(even + SPREAD_KERNEL) * share > SPREAD_MOST ? bytes
+                                                                                                 : std::max(bytes, even);
 }
 
 template <typename T, int HD, int KT>
@@ -1428,7 +1424,7 @@ cudaError_t part_hd(bool back, const DecayArgs& a, const void* x0, const void* y
   TileMaps m0, m1;
   if (!tile_maps<T, HD>(&m0, a, x0, y0, nullptr, nullptr) || !tile_maps<T, HD>(&m1, a, x1, y1, nullptr, nullptr))
     return cudaErrorInvalidValue;
-  cudaError_t e = allow_smem<decay_part_kernel<T, HD, KT>>(bytes);
+  cudaError_t e = allow_smem<decay_part_kernel<T, HD, KT>, std::max(part_smem<T, HD>(), spread_even(1))>();
   if (e != cudaSuccess) return e;
   return launch_k(decay_part_kernel<T, HD, KT>, grid, dim3(CH_THREADS), bytes, s, m0, m1, a, (const T*)x0,
                   (const T*)y0, (const T*)x1, (const T*)y1);
@@ -1441,7 +1437,7 @@ cudaError_t pass_hd(int n_items, const DecayArgs& a, const void* p0, const void*
   const int bytes = spread_smem(pass_smem<T, HD, BACK>(), grid.x);
   TileMaps m;
   if (!tile_maps<T, HD>(&m, a, p0, p1, p2, p3)) return cudaErrorInvalidValue;
-  cudaError_t e = allow_smem<decay_pass_kernel<T, HD, KT, BACK>>(bytes);
+  cudaError_t e = allow_smem<decay_pass_kernel<T, HD, KT, BACK>, std::max(pass_smem<T, HD, BACK>(), spread_even(1))>();
   if (e != cudaSuccess) return e;
   return launch_k(decay_pass_kernel<T, HD, KT, BACK>, grid, dim3(PassShape<T, HD, BACK>::THREADS), bytes, s, m, a,
                   (const T*)p0, (const T*)p1, (const T*)p2, (const T*)p3, (T*)out0, (T*)out1);

@@ -5,6 +5,8 @@ what a caller may do with streams, states and workspaces.
 u16 = 2^-8 and u32 = 2^-24 are half a step of bf16 and fp32, M the same sum with
 every term by its absolute value.
 """
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -375,3 +377,39 @@ def test_decay_histories_that_are_not_cut(cuda, dtype, hd, lengths):
     assert set(names) - {"decay_prep"} == {"decay_pass"}
     _, names = _launched(lambda: R.decay_attn_backward(*t, cu, heads, ts=tts))
     assert set(names) - {"decay_prep"} == {"decay_pass", "decay_dkdv"}
+
+
+# ---------------------------------------------------------------- threads
+
+
+def test_decay_calls_from_several_threads(cuda):
+    """Batches whose launches take different amounts of shared memory, each from a
+    thread and stream of its own: no call refused, the same bits as alone."""
+    heads = R.DecayHeads((0, 0, 0, 0), (-0.1, -0.01, -0.3, 0.0), 64)
+    torch.manual_seed(4)
+    cases = []
+    for lengths in ((64,), (300,) * 10, (64,) * 148, (640,) * 3, (70,) * 300, (5000,)):
+        cu = np.concatenate([[0], np.cumsum(lengths)]).astype(np.int32)
+        x = [torch.randn(int(cu[-1]), 256, device=cuda).bfloat16() for _ in range(4)]
+        cases.append((cu, x, R.decay_attn_forward(*x[:3], cu, heads), R.decay_attn_backward(*x, cu, heads)))
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(cu, x, o, grads):
+        try:
+            stream = torch.cuda.Stream()
+            for _ in range(40):
+                got = R.decay_attn_forward(*x[:3], cu, heads, stream=stream)
+                back = R.decay_attn_backward(*x, cu, heads, stream=stream)
+                stream.synchronize()
+                if not torch.equal(got, o) or not all(torch.equal(a, b) for a, b in zip(back, grads)):
+                    wrong.append("other bits")
+        except Exception as e:  # noqa: BLE001
+            wrong.append(repr(e))
+
+    threads = [threading.Thread(target=work, args=c) for c in cases]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, wrong[:3]
