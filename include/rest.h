@@ -416,7 +416,9 @@ rest_status rest_embed_backward(rest_dtype dt, long long n_rows, int d, const vo
  * T is below 2^30 (REST_ERR_UNSUPPORTED beyond). Outputs overlap no input. A
  * value that is not finite stays in its history: it reaches the rows that
  * depend on it and, since masked products are zeros times it, may reach the
- * other rows of its own 16 (rows 16 m .. 16 m + 15 of the history). */
+ * other rows of its own 16 (rows 16 m .. 16 m + 15 of the history). After
+ * REST_ERR_TIMEOUT the outputs are void, and so are the slots that the call
+ * continues. */
 
 /* Cached states, one slot per history, in caller-owned device memory (all four
  * arrays zero-filled describe n_slots empty histories). The calls read and
@@ -478,6 +480,16 @@ rest_status rest_decay_attn_step(rest_dtype dt, const rest_heads* heads, const d
                                  const void* q, const void* k, const void* v, const int64_t* ts,
                                  const rest_decay_state* state, const int32_t* slots, void* o, int32_t* dev_err,
                                  void* stream);
+
+/* The same as a failure-detection self-test (no GPU fault): its copies of the
+ * states count as arrived for no wait, and the waits give up after limit_cycles
+ * SM clock cycles (1e6 .. 4e9). Afterwards *dev_err (dev, required) holds
+ * REST_ERR_TIMEOUT, the state and o are as they were (nothing that did not arrive
+ * is stored or counted), and the context is usable. */
+rest_status rest_selftest_decay_step_timeout(rest_dtype dt, const rest_heads* heads, const double* log_decay, int n,
+                                             const void* q, const void* k, const void* v, const int64_t* ts,
+                                             const rest_decay_state* state, const int32_t* slots, void* o,
+                                             long long limit_cycles, int32_t* dev_err, void* stream);
 
 /* Failure-detection self-test (no GPU fault): launches n_ctas (1..1024) CTAs
  * whose threads wait, with the bounded wait every library kernel uses, on a

@@ -41,7 +41,8 @@ EXPORTS = ("rest_workspace_size", "rest_rotation_table", "rest_encoder_attn", "r
            "rest_append_workspace_size", "rest_encoder_append", "rest_attn_workspace_size", "rest_attn_forward",
            "rest_attn_backward", "rest_selftest_wait_timeout", "rest_static_ws_bytes", "rest_embed_forward",
            "rest_embed_workspace_size", "rest_embed_backward", "rest_decay_attn_workspace_size",
-           "rest_decay_attn_forward", "rest_decay_attn_backward", "rest_decay_attn_step")
+           "rest_decay_attn_forward", "rest_decay_attn_backward", "rest_decay_attn_step",
+           "rest_selftest_decay_step_timeout")
 
 
 class RestError(RuntimeError):
@@ -131,9 +132,10 @@ def _load() -> ctypes.CDLL:
     lib.rest_decay_attn_forward.argtypes = [c_int, P, P, P, P, P, P, P, P, P, P, P, c_size_t, P, P]
     lib.rest_decay_attn_backward.argtypes = [c_int, P, P, P, P, P, P, P, P, P, P, P, P, c_size_t, P, P]
     lib.rest_decay_attn_step.argtypes = [c_int, P, P, c_int, P, P, P, P, P, P, P, P, P]
+    lib.rest_selftest_decay_step_timeout.argtypes = [c_int, P, P, c_int, P, P, P, P, P, P, P, c_longlong, P, P]
     for name in ("rest_embed_forward", "rest_embed_workspace_size", "rest_embed_backward",
                  "rest_decay_attn_workspace_size", "rest_decay_attn_forward", "rest_decay_attn_backward",
-                 "rest_decay_attn_step"):
+                 "rest_decay_attn_step", "rest_selftest_decay_step_timeout"):
         getattr(lib, name).restype = c_int
     for name in ("rest_selftest_wait_timeout", "rest_workspace_size", "rest_rotation_table", "rest_encoder_attn",
                  "rest_cross_decode",
@@ -846,6 +848,22 @@ def selftest_wait_timeout(device, n_ctas: int = 148, limit_cycles: int = 20_000_
     _check(_lib.rest_selftest_wait_timeout(n_ctas, limit_cycles, _ptr(err), _stream(stream)),
            "rest_selftest_wait_timeout")
     return int(err.item())
+
+
+def selftest_decay_step_timeout(q, k, v, state: DecayState, o, ts=None, slots=None, limit_cycles: int = 2_000_000) -> int:
+    """``decay_attn_step`` whose waits for the states run out; returns the status
+    word it left (REST_ERR_TIMEOUT, 5, when detection works)."""
+    import torch
+    n, heads = q.shape[0], state.heads
+    dev, dt = _decay_inputs(n, heads, q, k, v, ts)
+    st, sl = _decay_slots(n, state, slots, heads, dev)
+    _expect("o", o, q.dtype, q.shape, dev)
+    err = torch.zeros(1, dtype=torch.int32, device=dev)
+    with torch.cuda.device(dev):
+        _check(_lib.rest_selftest_decay_step_timeout(dt, heads.heads, heads.decay, n, q.data_ptr(), k.data_ptr(),
+                                                     v.data_ptr(), _ptr(ts), st, sl, o.data_ptr(), limit_cycles,
+                                                     err.data_ptr(), _stream(None)), "rest_selftest_decay_step_timeout")
+        return int(err.item())
 
 
 def launch_count(reset: bool = False) -> int:

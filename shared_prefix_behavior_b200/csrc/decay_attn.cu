@@ -248,13 +248,14 @@ __device__ __forceinline__ void tma_tiles(uint32_t dst, const TileMaps& maps, in
 // Bounded wait for a phase of a barrier. Unlike the library's other waits it does
 // not give up once any error is on record: what these kernels report of a slot or
 // a timestamp leaves the outputs as documented. A timeout elsewhere does end it.
-__device__ __forceinline__ void wait_phase(uint64_t* bar, uint32_t parity, int32_t* err, volatile int* abort) {
+__device__ __forceinline__ void wait_phase(uint64_t* bar, uint32_t parity, int32_t* err, volatile int* abort,
+                                           long long limit = sm100::kWaitCycles) {
   if (sm100::mbar_try_wait(bar, parity)) return;
   const long long t0 = clock64();
   for (uint32_t n = 1; !sm100::mbar_try_wait(bar, parity); ++n) {
     if ((n & 127) != 0) continue;
     if (*abort) return;
-    const bool late = clock64() - t0 > sm100::kWaitCycles;
+    const bool late = clock64() - t0 > limit;
     if (late) set_error(err, REST_ERR_TIMEOUT);
     if (late || (err && *reinterpret_cast<volatile int32_t*>(err) == REST_ERR_TIMEOUT)) {
       *abort = 1;
@@ -267,10 +268,10 @@ __device__ __forceinline__ void wait_phase(uint64_t* bar, uint32_t parity, int32
 // later wait gives up at once), no more copies are started, and before the
 // block ends their issuer waits, as long as any wait may, for those in flight.
 template <int STAGES>
-__device__ __noinline__ void drain(uint64_t* full, int issued) {
+__device__ __noinline__ void drain(uint64_t* full, int issued, long long limit = sm100::kWaitCycles) {
   int none = 0;
   for (int i = issued > STAGES ? issued - STAGES : 0; i < issued; ++i)
-    sm100::mbar_wait_for(&full[i % STAGES], (i / STAGES) & 1, nullptr, &none, sm100::kWaitCycles);
+    sm100::mbar_wait_for(&full[i % STAGES], (i / STAGES) & 1, nullptr, &none, limit);
 }
 template <int HD, int THREADS>
 __device__ __forceinline__ void clear_rows(uint32_t tile, int from) {
@@ -1213,7 +1214,8 @@ template <typename T, int HD>
 __global__ void __launch_bounds__(STEP_THREADS, 4) decay_step_kernel(DecayHeadsArg hs, const T* __restrict__ q,
                                                                      const T* __restrict__ k,
                                                                      const T* __restrict__ v, const int64_t* ts,
-                                                                     DecayState st, T* o, float scale, int32_t* err) {
+                                                                     DecayState st, T* o, float scale,
+                                                                     DecayWait waits, int32_t* err) {
   constexpr int G = STEP_CHUNK / (HD * HD), C = HD / 4, R = HD / 4, PER = STEP_THREADS / G;  // threads per head
   constexpr int LANES_R = 32 / C < R ? 32 / C : R;  // row groups of a head within a warp
   extern __shared__ __align__(128) float chunk[];   // [STEP_STAGES][STEP_CHUNK]
@@ -1224,7 +1226,7 @@ __global__ void __launch_bounds__(STEP_THREADS, 4) decay_step_kernel(DecayHeadsA
   const int tid = threadIdx.x;
   if (tid == 0) {
     abort_flag = 0;
-    for (int i = 0; i < STEP_STAGES; ++i) sm100::mbar_init(&full[i], 1);
+    for (int i = 0; i < STEP_STAGES; ++i) sm100::mbar_init(&full[i], 1 + waits.missing);
     sm100::fence_mbar_init();
   }
   pdl_wait();
@@ -1248,8 +1250,9 @@ __global__ void __launch_bounds__(STEP_THREADS, 4) decay_step_kernel(DecayHeadsA
                  : "memory");
   };
   // read even before it is known whether the slot holds anything: what an empty slot has is not used
+  int issued = min(mine, STEP_STAGES);
   if (tid == 0)
-    for (int i = 0; i < min(mine, STEP_STAGES); ++i) load(i);
+    for (int i = 0; i < issued; ++i) load(i);
   long long len = 0, t = 0, t_first = 0, t_last = 0;
   if (in) {
     len = st.len[slot];
@@ -1272,6 +1275,7 @@ __global__ void __launch_bounds__(STEP_THREADS, 4) decay_step_kernel(DecayHeadsA
   bad = __syncthreads_or(bad);
   // every block of the cluster has read the bookkeeping once all have arrived
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  auto stopped = [&] { return *reinterpret_cast<volatile int*>(&abort_flag) != 0; };
   const int g = tid / PER, r = tid % PER / C, c = tid % C;
   for (int i = 0; i < mine; ++i) {
     const int h0 = head0(i), h = h0 + g;
@@ -1286,7 +1290,7 @@ __global__ void __launch_bounds__(STEP_THREADS, 4) decay_step_kernel(DecayHeadsA
         qq[y] = to_f(q[at + r + y * R]);
       }
     }
-    wait_phase(&full[i % STEP_STAGES], (i / STEP_STAGES) & 1, err, &abort_flag);
+    wait_phase(&full[i % STEP_STAGES], (i / STEP_STAGES) & 1, err, &abort_flag, waits.limit);
     if (bad) {  // nothing but the loads that are on their way
       if (i + 1 == min(mine, STEP_STAGES)) break;
       continue;
@@ -1315,6 +1319,9 @@ __global__ void __launch_bounds__(STEP_THREADS, 4) decay_step_kernel(DecayHeadsA
     if (r % LANES_R == 0) store4(&part[tid / C][4 * c], acc);
     sm100::fence_async_smem();
     __syncthreads();
+    // A wait ran out: what the chunk holds is not the state and stays here. All
+    // threads see the same, since none waits again before the next barrier.
+    if (stopped()) break;
     if (tid == 0) {
       asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
                        states + (size_t)h0 * (HD * HD)),
@@ -1324,6 +1331,7 @@ __global__ void __launch_bounds__(STEP_THREADS, 4) decay_step_kernel(DecayHeadsA
       if (i >= 1 && i - 1 + STEP_STAGES < mine) {  // the chunk before has left its buffer
         sm100::bulk_wait_read<1>();
         load(i - 1 + STEP_STAGES);
+        issued = i + STEP_STAGES;
       }
     }
     for (int y = tid; y < G * HD; y += STEP_THREADS) {
@@ -1337,11 +1345,15 @@ __global__ void __launch_bounds__(STEP_THREADS, 4) decay_step_kernel(DecayHeadsA
     }
     if (i + 1 < mine) __syncthreads();  // the sums are read
   }
-  if (tid == 0) sm100::bulk_wait<0>();
+  if (tid == 0) {
+    if (stopped()) drain<STEP_STAGES>(full, issued, waits.limit);
+    sm100::bulk_wait<0>();
+  }
+  __syncwarp();
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   if (rank == 0 && tid == 0) {
     if (bad) set_error(err, REST_ERR_INVALID_ARG);
-    if (in && !bad) {
+    if (in && !bad && !stopped()) {
       st.len[slot] = len + 1;
       if (ts) {
         if (t < t_last) set_error(err, REST_ERR_UNSORTED_TIME);
@@ -1362,7 +1374,7 @@ cudaError_t allow_smem() {
 
 template <typename T, int HD>
 cudaError_t step_hd(const DecayHeadsArg& hs, int n, const void* q, const void* k, const void* v, const int64_t* ts,
-                    const DecayState& st, void* o, float scale, int32_t* err, cudaStream_t s) {
+                    const DecayState& st, void* o, float scale, const DecayWait& waits, int32_t* err, cudaStream_t s) {
   // Blocks of an entry: as many as its chunks while they do not fill the GPU
   // (four blocks an SM).
   constexpr int G = STEP_CHUNK / (HD * HD), bytes = STEP_STAGES * STEP_CHUNK * 4;
@@ -1386,7 +1398,7 @@ cudaError_t step_hd(const DecayHeadsArg& hs, int n, const void* q, const void* k
   cfg.attrs = attr;
   cfg.numAttrs = pdl_enabled() ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, decay_step_kernel<T, HD>, hs, (const T*)q, (const T*)k, (const T*)v, ts, st, (T*)o,
-                            scale, err);
+                            scale, waits, err);
 }
 
 template <typename T, int HD>
@@ -1506,15 +1518,15 @@ cudaError_t launch_decay_dkdv(bool bf, int hd, int n_items, const DecayArgs& a, 
 
 cudaError_t launch_decay_step(bool bf, int hd, const DecayHeadsArg& hs, int n, const void* q, const void* k,
                               const void* v, const int64_t* ts, const DecayState& st, void* o, float scale,
-                              int32_t* err, cudaStream_t s) {
+                              const DecayWait& waits, int32_t* err, cudaStream_t s) {
   if (bf) {
-    if (hd == 16) return step_hd<bf16, 16>(hs, n, q, k, v, ts, st, o, scale, err, s);
-    if (hd == 32) return step_hd<bf16, 32>(hs, n, q, k, v, ts, st, o, scale, err, s);
-    return step_hd<bf16, 64>(hs, n, q, k, v, ts, st, o, scale, err, s);
+    if (hd == 16) return step_hd<bf16, 16>(hs, n, q, k, v, ts, st, o, scale, waits, err, s);
+    if (hd == 32) return step_hd<bf16, 32>(hs, n, q, k, v, ts, st, o, scale, waits, err, s);
+    return step_hd<bf16, 64>(hs, n, q, k, v, ts, st, o, scale, waits, err, s);
   }
-  if (hd == 16) return step_hd<float, 16>(hs, n, q, k, v, ts, st, o, scale, err, s);
-  if (hd == 32) return step_hd<float, 32>(hs, n, q, k, v, ts, st, o, scale, err, s);
-  return step_hd<float, 64>(hs, n, q, k, v, ts, st, o, scale, err, s);
+  if (hd == 16) return step_hd<float, 16>(hs, n, q, k, v, ts, st, o, scale, waits, err, s);
+  if (hd == 32) return step_hd<float, 32>(hs, n, q, k, v, ts, st, o, scale, waits, err, s);
+  return step_hd<float, 64>(hs, n, q, k, v, ts, st, o, scale, waits, err, s);
 }
 
 }  // namespace rest

@@ -100,6 +100,11 @@ struct DecayArgs {
   float scale;     // 1 / sqrt(head_dim)
   int32_t* err;
 };
+// The step's bounded waits: their limit in cycles, and arrivals that never come (the self-test's).
+struct DecayWait {
+  long long limit;
+  int missing;
+};
 cudaError_t launch_decay_prep(const DecayUsers& users, const int64_t* ts, const DecayState& st, const DecayArgs& a,
                               DecayItem* items, DecayPart* parts, DecayUser* heads, cudaStream_t s);
 // Every part's own state sum_j decay x0_j y0_j^T; with back also sum_i decay x1_i y1_i^T from the other side.
@@ -114,6 +119,6 @@ cudaError_t launch_decay_dkdv(bool bf16, int hd, int n_items, const DecayArgs& a
                               const void* v, const void* d_o, void* dk, void* dv, cudaStream_t s);
 cudaError_t launch_decay_step(bool bf16, int hd, const DecayHeadsArg& hs, int n, const void* q, const void* k,
                               const void* v, const int64_t* ts, const DecayState& st, void* o, float scale,
-                              int32_t* err, cudaStream_t s);
+                              const DecayWait& waits, int32_t* err, cudaStream_t s);
 
 }  // namespace rest

@@ -15,6 +15,7 @@
 #include "kernels.h"
 #include "rest.h"
 #include "sm100.h"
+#include "sm100_common.cuh"
 
 namespace rest {
 
@@ -1782,10 +1783,9 @@ rest_status rest_decay_attn_backward(rest_dtype dt, const rest_heads* heads, con
   }
 }
 
-rest_status rest_decay_attn_step(rest_dtype dt, const rest_heads* heads, const double* log_decay, int n,
-                                 const void* q, const void* k, const void* v, const int64_t* ts,
-                                 const rest_decay_state* state, const int32_t* slots, void* o, int32_t* dev_err,
-                                 void* stream) {
+static rest_status decay_step(rest_dtype dt, const rest_heads* heads, const double* log_decay, int n, const void* q,
+                              const void* k, const void* v, const int64_t* ts, const rest_decay_state* state,
+                              const int32_t* slots, void* o, const DecayWait& waits, int32_t* dev_err, void* stream) {
   try {
     DecayHeadsArg hs;
     DecayState cached;
@@ -1804,11 +1804,27 @@ rest_status rest_decay_attn_step(rest_dtype dt, const rest_heads* heads, const d
     const double per = (double)heads->n_heads * heads->head_dim * heads->head_dim, e = (double)dt_size(dt);
     REST_KLAUNCH(s, "decay_step", 5.0 * n * per, n * (8 * per + 4 * heads->d * e + 52),
                  launch_decay_step(dt == REST_BF16, heads->head_dim, hs, n, q, k, v, ts, cached, o,
-                                   (float)(1.0 / sqrt((double)heads->head_dim)), dev_err, s));
+                                   (float)(1.0 / sqrt((double)heads->head_dim)), waits, dev_err, s));
     return REST_OK;
   } catch (...) {
     return REST_ERR_INVALID_ARG;
   }
+}
+
+rest_status rest_decay_attn_step(rest_dtype dt, const rest_heads* heads, const double* log_decay, int n,
+                                 const void* q, const void* k, const void* v, const int64_t* ts,
+                                 const rest_decay_state* state, const int32_t* slots, void* o, int32_t* dev_err,
+                                 void* stream) {
+  return decay_step(dt, heads, log_decay, n, q, k, v, ts, state, slots, o, DecayWait{sm100::kWaitCycles, 0}, dev_err,
+                    stream);
+}
+
+rest_status rest_selftest_decay_step_timeout(rest_dtype dt, const rest_heads* heads, const double* log_decay, int n,
+                                             const void* q, const void* k, const void* v, const int64_t* ts,
+                                             const rest_decay_state* state, const int32_t* slots, void* o,
+                                             long long limit_cycles, int32_t* dev_err, void* stream) {
+  if (limit_cycles < 1000000LL || limit_cycles > 4000000000LL || !dev_err) return REST_ERR_INVALID_ARG;
+  return decay_step(dt, heads, log_decay, n, q, k, v, ts, state, slots, o, DecayWait{limit_cycles, 1}, dev_err, stream);
 }
 
 }  // extern "C"

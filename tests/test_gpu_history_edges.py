@@ -413,3 +413,36 @@ def test_decay_calls_from_several_threads(cuda):
     for t in threads:
         t.join()
     assert not wrong, wrong[:3]
+
+
+# ---------------------------------------------------------------- waits that run out
+
+
+def _step_case(cuda, dtype, hd, H, n):
+    torch.manual_seed(n)
+    heads = R.DecayHeads(([0, 64] * 16)[:H], [-0.1] * H, hd)
+    state = R.DecayState(heads, n + 1, device=cuda)
+    state.s.normal_()
+    state.len.fill_(3)
+    state.t_first.fill_(1000)
+    state.t_last.fill_(2000)
+    x = [torch.randn(n, H * hd, device=cuda).to(DT[dtype]) for _ in range(3)]
+    slots = torch.randperm(n + 1, device=cuda)[:n].int()
+    return x, state, torch.full((n,), 2500, device=cuda), slots
+
+
+@pytest.mark.parametrize("dtype,hd,H,n", [("bf16", 64, 8, 3), ("f32", 16, 2, 1), ("bf16", 32, 32, 40), ("f32", 64, 8, 700)])
+def test_a_step_whose_waits_run_out_leaves_its_state(cuda, dtype, hd, H, n):
+    """One block and several to an entry, one chunk and several to a block: nothing
+    of a chunk that did not arrive is stored, no token is counted, and the next
+    call is right."""
+    x, state, ts, slots = _step_case(cuda, dtype, hd, H, n)
+    kept = [t.clone() for t in (state.s, state.len, state.t_first, state.t_last)]
+    o = torch.full_like(x[0], 7.0)
+    assert R.selftest_decay_step_timeout(*x, state, o, ts=ts, slots=slots) == 5
+    assert all(torch.equal(a, b) for a, b in zip((state.s, state.len, state.t_first, state.t_last), kept))
+    assert torch.all(o == 7.0)
+    fresh = R.DecayState(state.heads, n + 1, tensors=kept)
+    want = R.decay_attn_step(*x, fresh, ts=ts, slots=slots)
+    assert torch.equal(R.decay_attn_step(*x, state, ts=ts, slots=slots), want)
+    assert torch.equal(state.s, fresh.s) and torch.equal(state.len, fresh.len)

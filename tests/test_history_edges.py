@@ -56,3 +56,18 @@ def test_the_smallest_workspace(lengths, back):
     assert _pass(back, ws_bytes=least - 256, **kw) == WORKSPACE
     heads = R.DecayHeads(taus, (-0.1, -0.1), 32)
     assert R.decay_attn_workspace_size(R.REST_BF16, heads, _cu(lengths)) >= least
+
+
+def test_the_step_self_test_refuses_its_limits():
+    import ctypes
+    from tests.test_history_boundary import FAKE, INVALID, _heads, _state
+    t, hs = _heads((0, 64), 16)
+    g = np.asarray((-0.1, 0.0))
+    st = _state()
+
+    def call(limit=2_000_000, err=FAKE):
+        return R.library().rest_selftest_decay_step_timeout(R.REST_F32, ctypes.byref(hs), g.ctypes.data, 0, None, None, None,
+                                                            FAKE, ctypes.byref(st), FAKE, None, limit, err, None)
+    assert call(limit=10) == call(limit=5_000_000_000) == call(err=None) == INVALID
+    if not gpu_available():
+        assert call() == NO_DEVICE
