@@ -417,8 +417,8 @@ rest_status rest_embed_backward(rest_dtype dt, long long n_rows, int d, const vo
  * value that is not finite stays in its history: it reaches the rows that
  * depend on it and, since masked products are zeros times it, may reach the
  * other rows of its own 16 (rows 16 m .. 16 m + 15 of the history). After
- * REST_ERR_TIMEOUT the outputs are void, and so are the slots that the call
- * continues. */
+ * REST_ERR_TIMEOUT, which takes the place of any other code, the outputs are
+ * void, and so are the slots that the call continues. */
 
 /* Cached states, one slot per history, in caller-owned device memory (all four
  * arrays zero-filled describe n_slots empty histories). The calls read and

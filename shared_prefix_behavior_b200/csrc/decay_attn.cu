@@ -247,7 +247,8 @@ __device__ __forceinline__ void tma_tiles(uint32_t dst, const TileMaps& maps, in
 }
 // Bounded wait for a phase of a barrier. Unlike the library's other waits it does
 // not give up once any error is on record: what these kernels report of a slot or
-// a timestamp leaves the outputs as documented. A timeout elsewhere does end it.
+// a timestamp leaves the outputs as documented. A timeout elsewhere does end it,
+// and takes the place of such a report, since it voids the outputs.
 __device__ __forceinline__ void wait_phase(uint64_t* bar, uint32_t parity, int32_t* err, volatile int* abort,
                                            long long limit = sm100::kWaitCycles) {
   if (sm100::mbar_try_wait(bar, parity)) return;
@@ -256,7 +257,7 @@ __device__ __forceinline__ void wait_phase(uint64_t* bar, uint32_t parity, int32
     if ((n & 127) != 0) continue;
     if (*abort) return;
     const bool late = clock64() - t0 > limit;
-    if (late) set_error(err, REST_ERR_TIMEOUT);
+    if (late && err) atomicExch(reinterpret_cast<int*>(err), REST_ERR_TIMEOUT);
     if (late || (err && *reinterpret_cast<volatile int32_t*>(err) == REST_ERR_TIMEOUT)) {
       *abort = 1;
       return;

@@ -446,3 +446,15 @@ def test_a_step_whose_waits_run_out_leaves_its_state(cuda, dtype, hd, H, n):
     want = R.decay_attn_step(*x, fresh, ts=ts, slots=slots)
     assert torch.equal(R.decay_attn_step(*x, state, ts=ts, slots=slots), want)
     assert torch.equal(state.s, fresh.s) and torch.equal(state.len, fresh.len)
+
+
+def test_a_timeout_is_reported_over_a_bad_slot(cuda):
+    """The bad slot's entry reports at once, the others' waits run out later: the
+    code that voids their outputs is the one that is left."""
+    x, state, ts, slots = _step_case(cuda, "bf16", 32, 8, 20)
+    slots[3] = 99
+    o = torch.full_like(x[0], 7.0)
+    assert R.selftest_decay_step_timeout(*x, state, o, ts=ts, slots=slots) == 5
+    with pytest.raises(R.RestError) as e:
+        R.decay_attn_step(*x, state, ts=ts, slots=slots)
+    assert e.value.status == 1
