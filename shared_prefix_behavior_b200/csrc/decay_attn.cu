@@ -1035,6 +1035,7 @@ __global__ void __launch_bounds__(PassShape<T, HD, BACK>::THREADS, pass_blocks<T
         block_sync<Q::THREADS>();
         clear_rows<HD, Q::THREADS>(t0 + (BACK ? 0 : PLANE), rows);
         clear_rows<HD, Q::THREADS>(t0 + (BACK ? PLANE : 2 * PLANE), rows);
+        if (BACK) sm100::fence_async_smem();  // every warp's zeros lie where TMA writes three steps on
         block_sync<Q::THREADS>();
       }
     } else {

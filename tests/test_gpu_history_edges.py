@@ -458,3 +458,24 @@ def test_a_timeout_is_reported_over_a_bad_slot(cuda):
     with pytest.raises(R.RestError) as e:
         R.decay_attn_step(*x, state, ts=ts, slots=slots)
     assert e.value.status == 1
+
+
+# ---------------------------------------------------------------- tiles that are filled again
+
+
+@pytest.mark.parametrize("hd", [16, 32, 64])
+def test_decay_gradients_of_ragged_ends_repeat(cuda, hd):
+    """Uncut histories of six blocks, the last of 13 rows: the backward pass starts
+    there, with zeros written into tiles that are filled again three blocks on.
+    Equal calls give equal bits, and each history's are those of its own batch."""
+    torch.manual_seed(hd)
+    H, n, L = 8, 90, 333
+    heads = R.DecayHeads((0,) * H, (-0.01,) * H, hd)
+    x = [torch.randn(n * L, H * hd, device=cuda).bfloat16() for _ in range(4)]
+    cu = np.arange(n + 1, dtype=np.int32) * L
+    least = torch.empty(R.decay_attn_workspace_size(R.REST_BF16, heads, [0] * (n + 1)), dtype=torch.uint8, device=cuda)
+    want = R.decay_attn_backward(*x, cu, heads, ws=least)
+    one = R.decay_attn_backward(*(t[:L] for t in x), cu[:2], heads, ws=least[:R.decay_attn_workspace_size(1, heads, [0, 0])])
+    assert all(torch.equal(a[:L], b) for a, b in zip(want, one))
+    for _ in range(50):
+        assert all(torch.equal(a, b) for a, b in zip(R.decay_attn_backward(*x, cu, heads, ws=least), want))
