@@ -573,15 +573,22 @@ def _expect_ws(ws, device) -> None:
         raise ValueError("ws must be contiguous")
 
 
+def _current_handle(device):
+    """The handle of ``device``'s current stream. Through torch's own shortcut where
+    it has one: building the Stream object takes 3 us, about as long as a launch."""
+    import torch
+    shortcut = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return torch.cuda.current_stream(device).cuda_stream if shortcut is None else shortcut(device.index)
+
+
 def _run(fn, device, stream, check: bool, err, *args) -> None:
     """fn(*args, err pointer, stream handle) with ``device`` current."""
     import torch
-    if device.index != torch._C._cuda_getDevice():
+    if device.index != torch.cuda.current_device():
         with torch.cuda.device(device):
             return _run(fn, device, stream, check, err, *args)
     if stream is None:
-        # the handle alone: building the Stream object around it takes 3 us, about as long as the launch
-        handle = torch._C._cuda_getCurrentRawStream(device.index)
+        handle = _current_handle(device)
     elif stream.device != device:
         raise ValueError(f"the stream is on {stream.device}, expected {device}")
     else:

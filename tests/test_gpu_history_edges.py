@@ -253,6 +253,22 @@ def test_a_call_allocates_on_its_stream(cuda, name, monkeypatch):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("name", CALLS)
+def test_calls_without_the_stream_shortcut(cuda, name, monkeypatch):
+    """torch's private names are a shortcut, not a need."""
+    call = _calls(cuda)[name]
+    want = call()
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        assert R._current_handle(torch.device("cuda", 0)) == side.cuda_stream
+        got = call()
+    torch.cuda.synchronize()
+    for a, b in zip(got if isinstance(got, tuple) else (got,), want if isinstance(want, tuple) else (want,)):
+        assert torch.equal(a, b)
+
+
 def test_outputs_on_another_stream_outlive_their_use_on_the_current_one(cuda):
     """Memory of an output that the current stream still reads is not handed out again by its own stream."""
     calls = _calls(cuda)
