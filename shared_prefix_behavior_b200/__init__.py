@@ -600,8 +600,9 @@ def _run(fn, device, stream, check: bool, err, *args) -> None:
         _expect("err", err, torch.int32, (1,), device)
         _check(fn(*args, err.data_ptr(), handle), fn.__name__)
         return
-    if torch.cuda.is_current_stream_capturing():
-        raise ValueError("a captured call cannot read its status back: pass check=False")
+    with torch.cuda.stream(stream):
+        if torch.cuda.is_current_stream_capturing():
+            raise ValueError("a captured call cannot read its status back: pass check=False")
     if err is None:
         err = _err_word(device, stream)
     else:

@@ -269,6 +269,27 @@ def test_calls_without_the_stream_shortcut(cuda, name, monkeypatch):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("name", ["embed_forward", "decay_attn_backward"])
+def test_a_captured_call_does_not_read_its_status(cuda, name):
+    """Refused whichever way the capturing stream is named, before anything is
+    enqueued: the capture goes on, and replays what check=False put there."""
+    call = _calls(cuda)[name]
+    want = call()
+    graph, side, calm = torch.cuda.CUDAGraph(), torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side, capture_error_mode="thread_local"):
+        with pytest.raises(ValueError, match="captured"):
+            call()
+        with torch.cuda.stream(calm):
+            with pytest.raises(ValueError, match="captured"):
+                call(stream=side)
+        got = call(check=False)
+    graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(got if isinstance(got, tuple) else (got,), want if isinstance(want, tuple) else (want,)):
+        assert torch.equal(a, b)
+
+
 def test_outputs_on_another_stream_outlive_their_use_on_the_current_one(cuda):
     """Memory of an output that the current stream still reads is not handed out again by its own stream."""
     calls = _calls(cuda)
