@@ -413,6 +413,13 @@ rest_status rest_embed_backward(rest_dtype dt, long long n_rows, int d, const vo
  * some number from 0 to 1 in place of exp(g_h (n_i - n_j)), and other histories
  * are not concerned.
  *
+ * Equal calls give equal bits. The rounding of the fp32 sums (before a bf16
+ * output's own rounding) depends on the segments that a history is cut into,
+ * which are chosen for the whole batch and the workspace given, and on whether
+ * states are passed: the carried state then has fp32 accuracy (1.5e-7), else in
+ * bf16 calls 2^-16. Calls that may run at the same time need workspaces of their
+ * own.
+ *
  * T is below 2^30 (REST_ERR_UNSUPPORTED beyond). Outputs overlap no input. A
  * value that is not finite stays in its history: it reaches the rows that
  * depend on it and, since masked products are zeros times it, may reach the

@@ -121,19 +121,18 @@ __device__ __forceinline__ DecayUser user_at(const DecayArgs& a, int u) {
 // block's last row and D the matrix exp(g (n_i - n_j)) for j <= i inside it:
 //   O = (D * (Q K^T)) V + diag(exp(g (n_i - n_0))) Q S
 //   S' = exp(g (n_1 - n_0)) S + (diag(exp(g (n_1 - n_j))) K)^T V
-// Every exponent is <= 0, however strong the decay. Exponents are formed in 64
-// bits and kept as a pair of floats, so that a difference of two nearby rows is
-// exact after a gap of years.
+// Every exponent that is used is <= 0, however strong the decay (over a decrease
+// of the timestamps it counts as 0). Exponents are formed in 64 bits and kept as a
+// pair of floats, within 2^-48 of themselves: a gap of 30 years in buckets of a
+// second leaves the rows after it their distances, at g = -1 to 4e-6.
 //
-// The products run on mma.sync (m16n8k16, bf16 in, fp32 out). The kernels move
-// 8 bytes per feature and row and multiply 4 or 5 times head_dim of them, so HBM
-// and the tensor pipe are near each other; measured here, mma.sync runs at
-// 545 TFLOP/s, and a warp issues a tcgen05.mma of M = 128 about every 107
-// cycles whatever its N and K = 16: with head_dim 64 a 128-row block needs 36 of
-// them, 3850 issue cycles, against 2180 cycles of mma.sync for the same rows.
-// The segments' own states on tcgen05, with their sums in TMEM, measured no less
-// than on mma.sync (2 x 16384 rows 30 us against 26, gradients of 8 x 4096 40
-// against 42): what decays the rows bounds both.
+// The products run on mma.sync (m16n8k16, bf16 in, fp32 out), which runs at
+// 545 TFLOP/s here. Of the three kernels only the segments' own states were tried
+// on tcgen05, with their sums in TMEM: no faster than mma.sync (2 x 16384 rows
+// 30 us against 26, gradients of 8 x 4096 40 against 42), since what decays the
+// rows bounds both. The pass, two thirds of the time, was not: one warp issues a
+// tcgen05.mma of M = 128 about every 107 cycles whatever its N, so it would want
+// several issuing warps.
 //
 // An operand is one bf16 number (bf16 calls) or the exact sum of three (fp32
 // calls: 8 + 8 + 8 significant bits), and a product sums the pairs of terms
@@ -670,7 +669,11 @@ __global__ void __launch_bounds__(JOIN_THREADS, 10) decay_join_kernel(const __gr
   }
 }
 
-// Blocks an SM holds: registers and shared memory together
+// Blocks an SM holds, which their registers are cut to. One number for both types:
+// bf16's, whose head_dim 32 and 64 passes have next to no spills at it. fp32 spills
+// up to 72 bytes; one block less, without spills, measured 287 us instead of 272
+// (forward, 8 x 4096 rows of 8 heads of 64), 271 instead of 251 (backward, 32 x
+// 1024 of 8 heads of 32), but 87 instead of 103 for the forward of the latter.
 template <typename T, int HD, bool BACK>
 __host__ __device__ constexpr int pass_blocks() { return HD < 64 ? (BACK ? 2 : 3) : BACK ? 1 : 2; }
 
@@ -730,11 +733,11 @@ __device__ __forceinline__ void store_rows(T* out, int d, uint32_t tile, const f
 // state's warps work out the next block's state, operand and decays while the
 // output's warps use this block's, and the tiles after it are on their way.
 // Barriers of three stages keep them apart; no warp waits for another's rows.
-// (All of it in the same four warps measured 57 us at 2 x 16384 rows of 8 heads
-// of 64, one latency after the other; now 40 us.) There the
-// tensor pipe is busy 31 % of the time, shared memory's wavefronts 54 % and the
-// issue slots 43 %, HBM 34 %: the mix of products, fragment loads, weights and
-// roundings bounds it, no one of them alone.
+// (With operands of one term, all of it in the same four warps measured 57 us at
+// 2 x 16384 rows of 8 heads of 64, one latency after the other, and 40 so.) Now 53
+// us: the tensor pipe is busy 48 % of the time, shared memory's wavefronts 52 % and
+// the issue slots 45 %, HBM 2.1 TB/s: the mix of products, fragment loads, weights
+// and roundings bounds it, no one of them alone.
 //
 // Forward, and for dq with dO, V, K in the places of Q, K, V:
 //   O = (D * (Q K^T)) V + diag(exp(g (n_i - n_0))) Q S,  n_0 the index before the block

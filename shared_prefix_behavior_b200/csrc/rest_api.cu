@@ -1544,9 +1544,11 @@ static size_t decay_layout(const rest_heads* hs, int n_users, bool back, long lo
 
 // A kernel's time in us: a 64-row block takes one resident CTA `alone` and each of
 // `per_sm` together `full`, and a CTA `fixed` besides (its first loads, the state
-// in and out). The numbers are fitted to 2,185 calls of given segments (117
-// shapes of 1 to 64 histories of 64 to 16384 rows, forward and backward); what they
-// choose is on average 1.6 % off the fastest of a shape's segments, 21 % at most.
+// in and out). The numbers are fitted to calls of given segments (117 shapes of 1 to
+// 64 histories of 64 to 16384 rows, forward and backward). The bf16 ones, fitted
+// before scores and states had two terms, were measured again with them (1,167
+// calls, 61 shapes): what they choose is on average 0.8 % off the fastest of a
+// shape's segments, 15 % at most; fp32 1.1 % and 16 % over 56 shapes when fitted.
 struct DecayCost { int per_sm; double alone, full, fixed; };
 // The CTAs of a launch, with their 64-row blocks: of full segments, and of those that end a history before.
 struct DecayLoad { double full, shorts, rows, short_blocks, longest_short; };
