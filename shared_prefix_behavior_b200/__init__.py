@@ -852,10 +852,11 @@ def selftest_wait_timeout(device, n_ctas: int = 148, limit_cycles: int = 20_000_
     """Runs the failure-detection self-test and returns the status word it left
     (REST_ERR_TIMEOUT, 5, when detection works)."""
     import torch
-    err = torch.zeros(1, dtype=torch.int32, device=device)
-    _check(_lib.rest_selftest_wait_timeout(n_ctas, limit_cycles, _ptr(err), _stream(stream)),
-           "rest_selftest_wait_timeout")
-    return int(err.item())
+    with torch.cuda.stream(stream):
+        err = torch.zeros(1, dtype=torch.int32, device=device)
+        _check(_lib.rest_selftest_wait_timeout(n_ctas, limit_cycles, _ptr(err), _stream(stream)),
+               "rest_selftest_wait_timeout")
+        return int(err.item())
 
 
 def selftest_decay_step_timeout(q, k, v, state: DecayState, o, ts=None, slots=None, limit_cycles: int = 2_000_000) -> int:

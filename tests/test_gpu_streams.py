@@ -1,6 +1,5 @@
 """Calls on a stream of their own: what they allocate is that stream's memory,
 and with ``check`` they wait for that stream before they read its status."""
-
 import pytest
 import torch
 
@@ -23,6 +22,11 @@ def test_the_status_is_read_on_the_calls_stream(cuda):
     with pytest.raises(R.RestError) as e:
         R.rotation_table(ts, [0, 3], (0, 1), 16, stream=other)
     assert e.value.status == 2
+
+
+def test_the_self_test_waits_for_its_stream(cuda):
+    assert R.selftest_wait_timeout(cuda, n_ctas=2, limit_cycles=20_000_000, stream=torch.cuda.Stream()) == 5
+
 
 def _calls(cuda):
     w = W.small_workload("bf16", lengths=(200, 37), d=128, n_heads=4, n_layers=1, l_switch=0,
